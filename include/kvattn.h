@@ -119,8 +119,14 @@ enum kvattn_device_error {
     KVATTN_DEVERR_PAGE_OUT_OF_RANGE = 1, /* block_table entry outside [0, num_pages): page skipped */
     KVATTN_DEVERR_SEQ_TOO_LONG = 2,      /* seq_lens[b] > max_seq_len: clamped to max_seq_len */
     KVATTN_DEVERR_WAIT_TIMEOUT = 4,      /* a bounded wait on an mbarrier ran out: tile skipped */
-    KVATTN_DEVERR_POS_OUT_OF_RANGE = 8   /* kvattn_append_kv: a position outside the sequence's
+    KVATTN_DEVERR_POS_OUT_OF_RANGE = 8,  /* kvattn_append_kv: a position outside the sequence's
                                             pages: that token skipped */
+    KVATTN_DEVERR_POOL_EXHAUSTED = 16,   /* kvattn_build_tables: too few free pages for a request:
+                                            it gets nothing */
+    KVATTN_DEVERR_TOO_MANY_TOKENS = 32,  /* kvattn_build_tables: more new tokens than max_tokens: the
+                                            request whose tokens do not fit gets nothing */
+    KVATTN_DEVERR_BAD_LENGTH = 64        /* a negative length or count, or chunk starts that fall or
+                                            leave their array: that request or sequence skipped */
 };
 
 /* Which decode kernel a plan uses. */
@@ -361,6 +367,160 @@ int kvattn_append_kv(int32_t variant, const kvattn_params *p, const void *new_kv
 int kvattn_head_proj(const void *x, const void *w, void *y, int32_t out_dtype, int32_t rows, int32_t heads,
                      int32_t k, int32_t n, int32_t *device_error, void *stream);
 
+/*
+ * The prompt side: many new tokens of every sequence at once.  The pages name
+ * the two forms of latent attention: the materialised per-head keys and values
+ * (MLA explainer section 2.3: k^C = W_UK c, v^C = c W_UV) and the absorbed one
+ * (MLRA page, MLA paragraph).  kvattn_decode is the absorbed form, for a few
+ * query tokens; the calls below give a step with ragged chunks its pages and
+ * slots, write its rows, expand the cached latents and attend them.  In one
+ * step: kvattn_build_tables, kvattn_append_slots, kvattn_expand_kv,
+ * kvattn_prefill; then kvattn_decode token by token on the same cache.
+ *
+ * A ragged batch packs its sequences' rows one after the other: sequence b has
+ * the rows [start[b], start[b + 1]) (int32 [batch + 1] on the device,
+ * ascending; batch <= 16384).  A sequence may have no rows.  Rows past the last
+ * sequence are not written.  Starts that fall or leave their array set
+ * KVATTN_DEVERR_BAD_LENGTH and the sequence is taken as empty.  device_error
+ * (int32 device word, may be NULL) collects kvattn_device_error bits; the
+ * caller clears it.
+ */
+
+/*
+ * kvattn_build_tables: block tables, positions and slots of a step, from the
+ * requests' lengths.  No page describes page management; serving engines on
+ * paged caches need it before every step.
+ *
+ * Request b has cached_lens[b] tokens in the cache, in the pages
+ * block_table[b][0 .. ceil(cached_lens[b] / 64)), and gets new_lens[b] more.
+ * The pages it lacks come off the top of the free list: free_pages int32
+ * [num_pages], of which the first *free_count hold free page ids; request by
+ * request, and in a request page by page, the last entry that is left is
+ * taken and written to the request's next place in block_table.  Other
+ * entries of the table stay as they are.  Written:
+ *   seq_lens  [batch]      cached_lens + new_lens
+ *   free_left [1]          entries left in the free list
+ *   q_start   [batch + 1]  first new token of each request in the packed batch
+ *   kv_start  [batch + 1]  the same over seq_lens (saturated at 2^31 - 1); may be NULL
+ *   pos, slots [max_tokens] for each new token its position in its sequence and
+ *                          its slot in the pool, page * 64 + pos % 64; slots past
+ *                          the last new token are -1 with pos 0 (a padded batch)
+ * seq_lens may be cached_lens, and free_left may be free_count: the call then
+ * updates them in place, and a captured step advances on each replay.  No other
+ * arrays may overlap.  To give pages back, write them behind the free list's
+ * last entry and raise the count, ordered before the next call.
+ *
+ * A request that cannot be served gets no pages, slots of -1 and its cached
+ * length, and its error bit is set: SEQ_TOO_LONG past max_pages_per_seq * 64
+ * tokens, POOL_EXHAUSTED where the free list ends (for it and for every later
+ * request that needs a page), TOO_MANY_TOKENS likewise where max_tokens ends
+ * (q_start stops there), BAD_LENGTH for a negative length (taken as 0).
+ * PAGE_OUT_OF_RANGE: a page id outside [0, num_pages), in the table or the free
+ * list; its tokens get slot -1.
+ * All pointers 4-byte aligned; batch <= 16384, num_pages < 2^25.
+ */
+int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int32_t num_pages, int32_t max_tokens,
+                        const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
+                        const int32_t *free_count, int32_t *block_table, int32_t *seq_lens, int32_t *free_left,
+                        int32_t *q_start, int32_t *kv_start, int32_t *pos, int32_t *slots, int32_t *device_error,
+                        void *stream);
+
+/*
+ * kvattn_append_slots: write num_tokens new rows into the paged cache by slot
+ * (kvattn_append_kv for ragged chunks).  p gives the cache geometry as for
+ * kvattn_append_kv, new_kv has its row layout: [num_tokens][num_kv*d_nope +
+ * d_rope] (latent), [num_tokens][2][num_kv][d_nope] (GQA/MQA),
+ * [num_tokens][num_kv][d_nope] (GTA), bf16.  slots int32 [num_tokens]: page *
+ * 64 + slot in the pool; -1 skips the token, any other value outside the pool
+ * sets KVATTN_DEVERR_PAGE_OUT_OF_RANGE and skips it.  Slots of one call are
+ * distinct.  rope_base > 1 turns k^R (latent) or every K head (GQA/MQA) at
+ * pos[token] (any value) exactly as kvattn_rope does; rope_base = 0 stores the
+ * rows as given (pos may be NULL; GTA takes only 0).
+ * cache_dtype FP8_E4M3 (GQA): keys (turned) are divided by k_scale and values
+ * by v_scale, rounded to the nearest e4m3 (ties to even) and saturated at
+ * +-448; NaN stays NaN.
+ * new_kv and kv_cache 16-byte aligned.
+ */
+int kvattn_append_slots(int32_t variant, const kvattn_params *p, const void *new_kv, int32_t num_tokens,
+                        const int32_t *pos, const int32_t *slots, void *kv_cache, float rope_base,
+                        int32_t *device_error, void *stream);
+
+/*
+ * kvattn_expand_kv: per-head keys and values of cached latents (MLA explainer
+ * section 2.3).  For every token j of every sequence of a ragged batch
+ * (kv_start over the cached tokens, token 0 first), with c_j the latent of head
+ * h's group:
+ *   k_nope[h][kv_start[b] + j] = W_UK[h] c_j      bf16 [H][max_kv_tokens][d_k]
+ *   v[h][kv_start[b] + j]      = c_j W_UV[h]      bf16 [H][max_kv_tokens][d_v]
+ *   k_rope[kv_start[b] + j]    = the cached k^R   bf16 [max_kv_tokens][d_rope]
+ * fp32 accumulation, one rounding to bf16 (nearest even).  Weights as for
+ * kvattn_head_proj: w_uk bf16 [H][d_k][d_nope], w_uv bf16 [H][d_nope][d_v].
+ * MLA and GLA (p: the cache geometry; batch = sequences, block_table as for
+ * decode; p->q_len and the split fields are not used).  d_nope a multiple of
+ * 64; d_k and d_v multiples of 8, at most 128.  A page id outside
+ * [0, num_pages) sets KVATTN_DEVERR_PAGE_OUT_OF_RANGE; its tokens' keys and
+ * values are 0.  k_rope may be NULL when d_rope == 0.
+ * workspace: kvattn_expand_workspace_size bytes, 256-byte aligned, in any
+ * state; calls that may run at the same time need one each.
+ */
+int kvattn_expand_workspace_size(int32_t variant, const kvattn_params *p, int32_t max_kv_tokens, size_t *bytes);
+int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cache, const int32_t *block_table,
+                     const int32_t *kv_start, int32_t max_kv_tokens, int32_t d_k, int32_t d_v, const void *w_uk,
+                     const void *w_uv, void *k_nope, void *v, void *k_rope, void *workspace, size_t workspace_bytes,
+                     int32_t *device_error, void *stream);
+
+/*
+ * kvattn_prefill: attention of ragged chunks of query tokens over per-head
+ * keys and values (the expanded form of latent attention; with d_rope = 0 plain
+ * grouped heads).  Sequence b has query rows [q_start[b], q_start[b + 1]) and
+ * key rows [kv_start[b], kv_start[b + 1]); head h reads key head h / (H / KH):
+ *   s_ij = sm_scale * (q_nope[i][h] . k_nope[h'][j] + q_rope[i][h] . k_rope[j])
+ *   out[i][h] = sum_j softmax_j(s_ij) v[h'][j],  lse[i][h] = ln sum_j exp(s_ij)
+ * causal = 1: query i of nq attends keys j <= i + nk - nq (the chunk is the
+ * newest nq of the sequence's nk tokens); a query without keys gives out = 0,
+ * lse = -inf.  causal = 0: every query attends every key.
+ *
+ * Strides in elements, {between tokens, between heads}; {0, 0} takes the dense
+ * layout: q_nope [T][H][d_nope], q_rope [T][H][d_rope], out [T][H][d_v], and
+ * head-major k [KH][max_kv_tokens][d_nope], v [KH][max_kv_tokens][d_v] (as
+ * kvattn_expand_kv writes them); k_rope [T][d_rope] has a token stride only.
+ * The last axis is contiguous; strides are multiples of 8; heads and tokens of
+ * out do not overlap.  lse (may be NULL) is fp32 [max_q_tokens][H].  bf16
+ * inputs; out bf16 (nearest even) or fp32.  d_nope and d_v multiples of 8 up to
+ * 128, d_rope of 8 up to 64.
+ * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded to
+ * bf16 for the product with v.  Key and value rows of other sequences and past
+ * the last one never reach a result, whatever they hold; inside a sequence
+ * values are taken to be finite (a value that is not may reach queries up to
+ * 127 tokens before it).
+ * workspace: kvattn_prefill_workspace_size bytes, 256-byte aligned, in any
+ * state; calls that may run at the same time need one each.
+ */
+typedef struct {
+    int32_t batch;             /* sequences, 1..16384 */
+    int32_t num_q_heads;       /* H */
+    int32_t num_kv_heads;      /* KH, divides H */
+    int32_t d_nope;
+    int32_t d_rope;            /* 0: no rope part (q_rope and k_rope unused) */
+    int32_t d_v;
+    int32_t max_q_tokens;      /* rows of q_nope, q_rope, out and lse (>= q_start[batch]) */
+    int32_t max_kv_tokens;     /* rows of k_nope, k_rope and v (>= kv_start[batch]) */
+    int32_t causal;            /* 0 or 1 */
+    int32_t out_dtype;         /* kvattn_out_dtype */
+    int64_t q_nope_stride[2];
+    int64_t q_rope_stride[2];
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int64_t out_stride[2];
+    int64_t k_rope_stride;
+} kvattn_prefill_params;
+
+int kvattn_prefill_workspace_size(const kvattn_prefill_params *p, size_t *bytes);
+int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope, const void *q_rope, const void *k_nope,
+                   const void *k_rope, const void *v, const int32_t *q_start, const int32_t *kv_start,
+                   float sm_scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                   int32_t *device_error, void *stream);
+
 /* Copy the device error word to *code (0 = none, else kvattn_device_error
  * bits).  Synchronises `stream`.  Returns KVATTN_ERR_CUDA if the copy
  * failed. */
@@ -369,9 +529,10 @@ int kvattn_get_device_error(const void *workspace, void *stream, int32_t *code);
 /* Static, human-readable name of a status code. */
 const char *kvattn_status_string(int status);
 
-/* Library ABI version (major * 100 + minor): 202 (kvattn_params carries q_len,
+/* Library ABI version (major * 100 + minor): 203 (kvattn_params carries q_len,
  * branch_out and the cache element type with its scales; the steps either side:
- * kvattn_rope, kvattn_append_kv, kvattn_head_proj). */
+ * kvattn_rope, kvattn_append_kv, kvattn_head_proj; the prompt side:
+ * kvattn_build_tables, kvattn_append_slots, kvattn_expand_kv, kvattn_prefill). */
 int kvattn_version(void);
 
 #ifdef __cplusplus

@@ -279,7 +279,7 @@ int validate_call(int32_t variant, const kvattn_params *p, const void *q_nope, c
 
 using namespace kvattn;
 
-extern "C" int kvattn_version(void) { return 202; }
+extern "C" int kvattn_version(void) { return 203; }
 
 extern "C" const char *kvattn_status_string(int status)
 {

@@ -1,0 +1,714 @@
+// Attention of ragged chunks of new tokens over per-head keys and values
+// (kvattn_prefill): the expanded form of latent attention, and grouped heads
+// without a rope part.
+//
+//   s_ij = sm_scale (q_nope_i . k_nope_j + q_rope_i . k_rope_j)
+//   o_i  = sum_j softmax_j(s_ij) v_j        over j < nk (causal: j <= i + nk - nq)
+//
+// One CTA works off 256 query rows of one head (two MMA tiles of 128) against
+// key tiles of 128 tokens in one pass with a running maximum and sum.  Per key
+// tile and query tile the tensor cores need 64 cycles for each 16 columns of
+// the key width and each 16 tokens of P.V (1280 cycles for 192 / 128) and the
+// special-function units 1024 cycles for 128 x 128 exponentials (16 per cycle
+// and SM), so the two query tiles take turns: while one's softmax runs, the
+// other's MMAs do.
+//
+// TMEM (512 columns): scores of the two tiles (128 each; the bf16
+// probabilities overwrite the first half), outputs of the two tiles (128
+// each).  Shared memory: the two query tiles, and a ring of 16 KB boxes (128
+// tokens x 64 columns, 128-byte swizzle) that key and value tiles pass through
+// in the order of their use.
+//
+// Warp roles (320 threads):
+//   warp 0     one thread streams queries, keys and values with TMA
+//   warp 1     one thread issues the MMAs, in the order
+//              S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
+//   warps 2-9  one thread per query row: scores from TMEM, mask, online softmax
+//              in fp32 (base 2), probabilities back to TMEM in bf16, output
+//              rescaled when the maximum grows by more than 2^8 (lazily: the
+//              reference maximum only scales numerator and denominator alike)
+// P is rounded to bf16 for the MMA (relative 2^-9, as in the decode kernels);
+// the sum uses the unrounded values; scores, maxima, sums and outputs stay in
+// fp32.
+//
+// The work list (tiles by falling number of keys) comes from ragged.cu; CTA c
+// of a grid of one CTA per SM takes items c, c + grid, ... of a list ordered
+// by groups of eight heads, then tiles, then heads, so that the CTAs at work
+// share a few heads' keys and values in L2.
+#include <math.h>
+
+#include "latent_common.cuh"
+#include "ragged.cuh"
+
+namespace kvattn {
+
+namespace {
+
+using latent::exp2_approx;
+using latent::fadd2;
+using latent::ffma2;
+using latent::kLn2;
+using latent::kRescaleThreshold;
+using latent::reduce_extreme;
+
+bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int kTile = 128;                        // query rows of an MMA tile, keys of a key tile
+constexpr int kItemRows = 2 * kTile;              // query rows of a work item
+constexpr int kThreads = 320;
+constexpr int kBoxBytes = kTile * 128;            // 128 rows x 64 bf16
+constexpr uint32_t kBoxUnits = kBoxBytes >> 4;
+constexpr int kHeadGroup = 8;
+constexpr int kBarBytes = 1024;
+constexpr int kSmemMax = 227 * 1024;
+
+struct PrefillArgs {
+    const int32_t *header;
+    const ragged::Tile *tiles;
+    void *out;
+    float *lse;                                   // may be null
+    int32_t *err;                                 // may be null
+    int heads, heads_per_kv;
+    int d_v, out_fp32, causal;
+    long long out_token_stride, out_head_stride;
+    float scale_log2;
+};
+
+struct Maps {
+    CUtensorMap q, qr, k, kr, v;
+};
+
+// NKB key boxes (the last one the rope part if ROPE), NVB value boxes.
+template <int NKB, int NVB>
+struct Layout {
+    static constexpr int kRing = (kSmemMax - kBarBytes - 2 * NKB * kBoxBytes) / kBoxBytes;
+    static constexpr int kStep = NKB + NVB;       // boxes of a key tile and its value tile
+    static constexpr size_t kBytes = (size_t)(2 * NKB + kRing) * kBoxBytes + kBarBytes;
+    static_assert(kRing >= 2 * NKB + NVB, "two key tiles and a value tile in flight");
+};
+
+struct Bars {
+    uint64_t full[16], empty[16];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier space");
+
+// Work item i: its tile, its head, and the key tiles of its two query tiles.
+struct Item {
+    ragged::Tile t;
+    int head;
+    int n0, n1;
+};
+
+__device__ __forceinline__ int key_end(const PrefillArgs &a, const ragged::Tile &t, int rows_before, int rows)
+{
+    // keys that the last of `rows` rows from rows_before on attends
+    if (rows <= 0)
+        return 0;
+    return a.causal ? min(t.nk, max(t.lim0 + rows_before + rows - 1, 0)) : t.nk;
+}
+
+__device__ __forceinline__ Item get_item(const PrefillArgs &a, int ntiles, int i)
+{
+    Item it;
+    const int per_group = ntiles * kHeadGroup;
+    const int g = i / per_group, r = i - g * per_group;
+    const int hc = min(kHeadGroup, a.heads - g * kHeadGroup);
+    it.t = a.tiles[r / hc];
+    it.head = g * kHeadGroup + r % hc;
+    it.n0 = (key_end(a, it.t, 0, min(it.t.nq, kTile)) + kTile - 1) / kTile;
+    it.n1 = (key_end(a, it.t, kTile, it.t.nq - kTile) + kTile - 1) / kTile;
+    return it;
+}
+
+template <int NKB, bool ROPE, int NVB>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ Maps m, const PrefillArgs a)
+{
+    using Lay = Layout<NKB, NVB>;
+    constexpr int R = Lay::kRing;
+    constexpr int NKN = ROPE ? NKB - 1 : NKB;
+    constexpr int kDv = NVB * 64;
+    constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile, false, false);
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(kTile, kDv, false, true);
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *const ring = smem + 2 * NKB * kBoxBytes;
+    Bars &B = *reinterpret_cast<Bars *>(ring + R * kBoxBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0 && a.err)
+            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < R; ++s) {
+            mbar_init(&B.full[s], 1);
+            mbar_init(&B.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.q_full[i], 1);
+            mbar_init(&B.q_empty[i], 1);
+            mbar_init(&B.s_full[i], 1);
+            mbar_init(&B.p_full[i], kTile);
+            mbar_init(&B.o_full[i], 1);
+        }
+        mbar_init(&B.mma_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0)
+        tmem_alloc(&B.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = B.tmem_base;
+    const uint32_t tS = tbase, tO = tbase + 2 * kTile;   // + kTile for the second query tile
+    pdl_wait_primary();                                  // the tile list
+    const int ntiles = a.header[0];
+    const int items = ntiles * a.heads;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA
+        if (lane == 0) {
+            uint32_t pos = 0;                            // boxes put into the ring
+            uint32_t qn[2] = {0, 0};                     // query tiles loaded
+            auto slot = [&]() -> int {
+                const int s = (int)(pos % R);
+                if (pos >= R && !mbar_wait(&B.empty[s], ((pos / R) - 1) & 1))
+                    ok = false;
+                return s;
+            };
+            auto load_q = [&](const Item &it, int i) {
+                if (qn[i] > 0 && !mbar_wait(&B.q_empty[i], (qn[i] - 1) & 1)) {
+                    ok = false;
+                    return;
+                }
+                ++qn[i];
+                mbar_arrive_expect_tx(&B.q_full[i], NKB * kBoxBytes);
+                const int row = it.t.q0 + i * kTile;
+#pragma unroll
+                for (int b = 0; b < NKB; ++b) {
+                    unsigned char *dst = smem + (i * NKB + b) * kBoxBytes;
+                    if (b < NKN)
+                        tma_load_3d(dst, &m.q, 64 * b, it.head, row, &B.q_full[i]);
+                    else
+                        tma_load_3d(dst, &m.qr, 0, it.head, row, &B.q_full[i]);
+                }
+            };
+            auto load_k = [&](const Item &it, int j) {
+                const int row = it.t.k0 + j * kTile, kvh = it.head / a.heads_per_kv;
+#pragma unroll
+                for (int b = 0; b < NKB; ++b) {
+                    const int s = slot();
+                    if (!ok)
+                        return;
+                    ++pos;
+                    mbar_arrive_expect_tx(&B.full[s], kBoxBytes);
+                    if (b < NKN)
+                        tma_load_3d(ring + s * kBoxBytes, &m.k, 64 * b, kvh, row, &B.full[s]);
+                    else
+                        tma_load_2d(ring + s * kBoxBytes, &m.kr, 0, row, &B.full[s]);
+                }
+            };
+            // The P.V descriptor steps from the first 64 columns' box to the
+            // next one's by a positive offset, so where the pair wraps around
+            // the ring the lower slot takes the first columns.
+            auto load_v = [&](const Item &it, int j) {
+                const int row = it.t.k0 + j * kTile, kvh = it.head / a.heads_per_kv;
+#pragma unroll
+                for (int b = 0; b < NVB; ++b) {
+                    const int s = slot();
+                    if (!ok)
+                        return;
+                    const bool wraps = NVB == 2 && (int)((pos - b) % R) == R - 1;
+                    ++pos;
+                    mbar_arrive_expect_tx(&B.full[s], kBoxBytes);
+                    tma_load_3d(ring + s * kBoxBytes, &m.v, 64 * (wraps ? 1 - b : b), kvh, row, &B.full[s]);
+                }
+            };
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item it = get_item(a, ntiles, i);
+                const int n = max(it.n0, it.n1);
+                if (n == 0)
+                    continue;
+                if (it.n0 > 0)
+                    load_q(it, 0);
+                if (ok)
+                    load_k(it, 0);
+                if (ok && it.n1 > 0)
+                    load_q(it, 1);
+                if (ok)
+                    load_v(it, 0);
+                for (int j = 1; ok && j < n; ++j) {
+                    load_k(it, j);
+                    if (ok)
+                        load_v(it, j);
+                }
+            }
+            // every copy started here has landed before the CTA can exit
+            for (int s = 0; s < R && s < (int)min(pos, (uint32_t)R); ++s) {
+                const uint32_t uses = (pos - 1 - s) / R;         // full phases before the slot's last
+                if (!mbar_wait(&B.full[s], uses & 1))
+                    ok = false;
+            }
+            for (int i = 0; i < 2; ++i)
+                if (qn[i] > 0 && !mbar_wait(&B.q_full[i], (qn[i] - 1) & 1))
+                    ok = false;
+            if (!ok && a.err)
+                atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA
+        const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);       // K-major query boxes
+        const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);       // K-major key boxes
+        uint32_t base = 0;                               // ring position of the item's first key tile
+        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};         // query tiles and probability tiles taken
+        auto wait_box = [&](uint32_t pos) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(&B.full[pos % R], (pos / R) & 1));
+        };
+        // scores of query tile i and key tile j; free: the last use of the keys
+        auto issue_s = [&](const Item &it, int i, int j, bool first, bool free) {
+            const uint32_t p0 = base + (uint32_t)j * Lay::kStep;
+            if (j == 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&B.q_full[i], qn[i] & 1))) {
+                    ok = false;
+                    return;
+                }
+                ++qn[i];
+            }
+#pragma unroll
+            for (int b = 0; b < NKB; ++b) {
+                if (first && !wait_box(p0 + b)) {
+                    ok = false;
+                    return;
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t s = (p0 + b) % R;
+                    const uint64_t qd = qdesc + (uint64_t)((i * NKB + b) * kBoxUnits);
+                    const uint64_t kd = kdesc + (uint64_t)(s * kBoxUnits);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_ss(tS + i * kTile, qd + k * 2, kd + k * 2, kIdescS, (b | k) ? 1u : 0u);
+                    if (free)
+                        umma_commit(&B.empty[s]);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) {
+                umma_commit(&B.s_full[i]);
+                if (j + 1 == (i ? it.n1 : it.n0))
+                    umma_commit(&B.q_empty[i]);
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](const Item &it, int i, int j, bool first, bool free) {
+            const uint32_t p0 = base + (uint32_t)j * Lay::kStep + NKB;
+            if (first) {
+#pragma unroll
+                for (int b = 0; b < NVB; ++b)
+                    if (!wait_box(p0 + b)) {
+                        ok = false;
+                        return;
+                    }
+                // value rows past the sequence are zeroed: their probabilities
+                // are 0, and 0 * NaN would poison the output
+                const int ntok = it.t.nk - j * kTile;
+                if (ntok < kTile) {
+                    for (int idx = lane; idx < (kTile - ntok) * 8 * NVB; idx += 32) {
+                        const int b = idx / ((kTile - ntok) * 8), rem = idx % ((kTile - ntok) * 8);
+                        *reinterpret_cast<uint4 *>(ring + ((p0 + b) % R) * kBoxBytes + (ntok + rem / 8) * 128 +
+                                                   (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&B.p_full[i], pn[i] & 1))) {
+                ok = false;
+                return;
+            }
+            ++pn[i];
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t s0 = p0 % R, s1 = (p0 + NVB - 1) % R;
+                const uint32_t lo = s0 < s1 ? s0 : s1, hi = s0 < s1 ? s1 : s0;
+                const uint64_t vd = smem_desc(smem_u32(ring) + lo * kBoxBytes,
+                                              NVB == 2 ? (hi - lo) * kBoxBytes : kBoxBytes, 1024, 2);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    umma_ts(tO + i * kTile, tS + i * kTile + 8 * k, vd + (uint64_t)(k * 128), kIdescPV,
+                            (j > 0 || k > 0) ? 1u : 0u);
+                if (free) {
+                    umma_commit(&B.empty[s0]);
+                    if (NVB == 2)
+                        umma_commit(&B.empty[s1]);
+                }
+                if (j + 1 == (i ? it.n1 : it.n0))
+                    umma_commit(&B.o_full[i]);
+            }
+            __syncwarp();
+        };
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item it = get_item(a, ntiles, i);
+            const int n = max(it.n0, it.n1);
+            if (it.n0 > 0)
+                issue_s(it, 0, 0, true, it.n1 == 0);
+            if (ok && it.n1 > 0)
+                issue_s(it, 1, 0, it.n0 == 0, true);
+            for (int j = 0; ok && j < n; ++j) {
+                const bool in0 = j < it.n0, in1 = j < it.n1, next0 = j + 1 < it.n0, next1 = j + 1 < it.n1;
+                if (in0)
+                    issue_pv(it, 0, j, true, !in1);
+                if (ok && next0)
+                    issue_s(it, 0, j + 1, true, !next1);
+                if (ok && in1)
+                    issue_pv(it, 1, j, !in0, true);
+                if (ok && next1)
+                    issue_s(it, 1, j + 1, !next0, true);
+            }
+            base += (uint32_t)n * Lay::kStep;
+        }
+        if (!ok && lane == 0 && a.err)
+            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+        // every MMA this thread issued has completed before TMEM is freed
+        if (lane == 0)
+            umma_commit(&B.mma_done);
+        __syncwarp();
+        if (!mbar_wait(&B.mma_done, 0) && lane == 0 && a.err)
+            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int i = (warp - 2) >> 2;                   // query tile
+        const int quarter = warp & 3;
+        const int row = i * kTile + quarter * 32 + lane; // of the item
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_addr = tS + i * kTile + lane_addr, o_addr = tO + i * kTile + lane_addr;
+        const bool flat = a.scale_log2 == 0.f;           // every key weighs the same
+        const float c = flat ? 1.f : a.scale_log2;
+        uint32_t sn = 0, on = 0;                         // score tiles and outputs taken
+        for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
+            const Item it = get_item(a, ntiles, w);
+            const int n = i ? it.n1 : it.n0;
+            const int lim = a.causal ? min(it.t.nk, it.t.lim0 + row) : it.t.nk;
+            const int lim_first = __shfl_sync(0xffffffffu, lim, 0);     // limits grow with the row
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&B.s_full[i], sn & 1));
+                if (!ok)
+                    break;
+                ++sn;
+                tc_fence_after();
+                float s[kTile];
+                {
+                    uint32_t r[kTile];
+                    tmem_ld128(s_addr, r);
+#pragma unroll
+                    for (int x = 0; x < kTile; ++x)
+                        s[x] = __uint_as_float(r[x]);
+                }
+                if (flat) {
+#pragma unroll
+                    for (int x = 0; x < kTile; ++x)
+                        s[x] *= 0.f;
+                }
+                // raw scores: the scale is folded into the exponent's FMA; for
+                // a negative scale the row's maximum is at the lowest score
+                const int nvalid = lim - j * kTile;
+                if (lim_first - j * kTile < kTile) {
+                    const float none = c >= 0.f ? -INFINITY : INFINITY;
+#pragma unroll
+                    for (int x = 0; x < kTile; ++x)
+                        s[x] = x < nvalid ? s[x] : none;
+                }
+                float mt;
+                if (c >= 0.f) {
+                    const float e = reduce_extreme<true, kTile>(s);
+                    mt = e == -INFINITY ? -INFINITY : c * e;
+                } else {
+                    const float e = reduce_extreme<false, kTile>(s);
+                    mt = e == INFINITY ? -INFINITY : c * e;
+                }
+                float alpha = 1.f;
+                bool rescale = false;
+                if (mt > m_ref + kRescaleThreshold) {
+                    if (m_ref != -INFINITY) {
+                        alpha = exp2f(m_ref - mt);
+                        rescale = true;
+                    }
+                    m_ref = mt;
+                }
+                const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                float sx[4] = {0.f, 0.f, 0.f, 0.f}, sy[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[kTile / 2];
+#pragma unroll
+                for (int x = 0; x < kTile / 2; ++x) {
+                    float x0, x1;
+                    ffma2(x0, x1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
+                    const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
+                    fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
+                    const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
+                    pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
+                }
+                l = l * alpha + (((sx[0] + sy[0]) + (sx[1] + sy[1])) + ((sx[2] + sy[2]) + (sx[3] + sy[3])));
+                tmem_st64(s_addr, pk);
+                // the scores' commit covers every earlier P.V, so the output
+                // holds all tiles before this one; TMEM accesses are
+                // warp-wide: the warp's rows are rescaled when any needs it
+                if (__any_sync(0xffffffffu, rescale)) {
+                    uint32_t r[32];
+#pragma unroll 1
+                    for (int x = 0; x < kDv / 32; ++x) {
+                        tmem_ld32(o_addr + 32 * x, r);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            r[y] = __float_as_uint(__uint_as_float(r[y]) * alpha);
+                        tmem_st32(o_addr + 32 * x, r);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&B.p_full[i]);
+            }
+            if (!ok)
+                break;
+            if (n > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&B.o_full[i], on & 1));
+                if (!ok)
+                    break;
+                ++on;
+                tc_fence_after();
+            }
+            const bool valid = row < it.t.nq;
+            const bool any = n > 0 && l != 0.f;          // a row without keys has l = 0 (NaN passes)
+            const float inv = any ? 1.f / l : 0.f;
+            const long long grow = (long long)it.t.q0 + row;
+            const long long at = grow * a.out_token_stride + it.head * a.out_head_stride;
+#pragma unroll 1
+            for (int x = 0; x < kDv; x += 32) {
+                uint32_t r[32];
+                if (n > 0)
+                    tmem_ld32(o_addr + x, r);
+#pragma unroll
+                for (int y = 0; y < 32; y += 8) {
+                    float f[8];
+#pragma unroll
+                    for (int z = 0; z < 8; ++z)
+                        f[z] = any ? __uint_as_float(r[y + z]) * inv : 0.f;
+                    if (!valid || x + y >= a.d_v) {
+                        // nothing to store
+                    } else if (a.out_fp32) {
+                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + x + y);
+                        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    } else {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(f[2 * z], f[2 * z + 1]);
+                            p[z] = *reinterpret_cast<const uint32_t *>(&v2);
+                        }
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at + x + y) =
+                            make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (valid && a.lse)
+                a.lse[grow * a.heads + it.head] = any ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+            // the next item's first P.V overwrites the output: it follows this
+            // warp's next arrival, which follows these loads
+            tc_fence_before();
+        }
+        if (!ok && lane == 0 && a.err)
+            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+    }
+    __syncwarp();
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        tmem_dealloc(tbase, 512);
+}
+
+struct Call {
+    Maps maps;
+    PrefillArgs args;
+    long long most_items;
+    cudaStream_t stream;
+};
+
+template <int NKB, bool ROPE, int NVB>
+cudaError_t launch(const Call &c)
+{
+    auto kern = prefill_kernel<NKB, ROPE, NVB>;
+    const size_t smem = Layout<NKB, NVB>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    const long long sms = sm_count();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(c.most_items < sms ? c.most_items : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, c.maps, c.args);
+}
+
+// Strides (elements) with the dense defaults filled in; false if one cannot be used.
+bool strides(const int64_t *given, long long token, long long head, long long *out)
+{
+    out[0] = given[0] ? given[0] : token;
+    out[1] = given[1] ? given[1] : head;
+    for (int i = 0; i < 2; ++i)
+        if (out[i] < 1 || out[i] % 8 || out[i] >= (1LL << 38))
+            return false;
+    return true;
+}
+
+// Tensor map of x [tokens][heads][d] in boxes of 128 tokens x 64 columns (zeros past d and past the last token).
+bool rows_map(CUtensorMap *map, const void *x, int d, int heads, long long tokens, const long long *st)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t bytes[2] = {(cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
+    const cuuint32_t box[3] = {64, 1, kTile};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, bytes, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+int validate_prefill(const kvattn_prefill_params *p)
+{
+    if (!p || p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->d_nope < 1 || p->d_rope < 0 ||
+        p->d_v < 1 || p->max_q_tokens < 0 || p->max_kv_tokens < 0 || (p->causal != 0 && p->causal != 1) ||
+        p->num_q_heads % p->num_kv_heads)
+        return KVATTN_ERR_INVALID_ARG;
+    if (p->out_dtype != KVATTN_OUT_BF16 && p->out_dtype != KVATTN_OUT_FP32)
+        return KVATTN_ERR_INVALID_ARG;
+    if (p->d_nope % 8 || p->d_rope % 8 || p->d_v % 8 || p->d_nope > 128 || p->d_rope > 64 || p->d_v > 128 ||
+        p->batch > ragged::kMaxBatch || p->num_q_heads > 65535)
+        return KVATTN_ERR_UNSUPPORTED;
+    const long long cap = ragged::tile_capacity(p->max_q_tokens, p->batch, kItemRows);
+    if (cap * ((p->num_q_heads + kHeadGroup - 1) / kHeadGroup * kHeadGroup) > INT32_MAX / 2)
+        return KVATTN_ERR_UNSUPPORTED;
+    return KVATTN_OK;
+}
+
+}  // namespace
+}  // namespace kvattn
+
+using namespace kvattn;
+
+extern "C" int kvattn_prefill_workspace_size(const kvattn_prefill_params *p, size_t *bytes)
+{
+    const int st = validate_prefill(p);
+    if (st)
+        return st;
+    if (!bytes)
+        return KVATTN_ERR_INVALID_ARG;
+    *bytes = ragged::kPlanHeader +
+             (size_t)ragged::tile_capacity(p->max_q_tokens, p->batch, kItemRows) * sizeof(ragged::Tile);
+    return KVATTN_OK;
+}
+
+extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope, const void *q_rope,
+                              const void *k_nope, const void *k_rope, const void *v, const int32_t *q_start,
+                              const int32_t *kv_start, float sm_scale, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, int32_t *device_error, void *stream)
+{
+    size_t need = 0;
+    const int st = kvattn_prefill_workspace_size(p, &need);
+    if (st)
+        return st;
+    if (!q_nope || !k_nope || !v || !q_start || !kv_start || !out || !workspace ||
+        (p->d_rope > 0 && (!q_rope || !k_rope)) || !isfinite(sm_scale))
+        return KVATTN_ERR_INVALID_ARG;
+    if (!is_aligned(q_nope, 16) || !is_aligned(q_rope, 16) || !is_aligned(k_nope, 16) || !is_aligned(k_rope, 16) ||
+        !is_aligned(v, 16) || !is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(workspace, 256) ||
+        !is_aligned(q_start, 4) || !is_aligned(kv_start, 4) || !is_aligned(device_error, 4))
+        return KVATTN_ERR_MISALIGNED;
+    if (workspace_bytes < need)
+        return KVATTN_ERR_WORKSPACE_TOO_SMALL;
+    const long long H = p->num_q_heads, KH = p->num_kv_heads, tq = p->max_q_tokens, tk = p->max_kv_tokens;
+    long long sq[2], sqr[2] = {8, 8}, sk[2], sv[2], so[2];
+    const int64_t kr_given[2] = {p->k_rope_stride, 8};
+    long long skr[2] = {8, 8};
+    if (!strides(p->q_nope_stride, H * p->d_nope, p->d_nope, sq) || !strides(p->k_stride, p->d_nope, tk * p->d_nope, sk) ||
+        !strides(p->v_stride, p->d_v, tk * p->d_v, sv) || !strides(p->out_stride, H * p->d_v, p->d_v, so) ||
+        (p->d_rope > 0 && (!strides(p->q_rope_stride, H * p->d_rope, p->d_rope, sqr) || !strides(kr_given, p->d_rope, 8, skr))))
+        return KVATTN_ERR_INVALID_ARG;
+    if (tq == 0)
+        return KVATTN_OK;
+
+    Call c;
+    Maps &m = c.maps;
+    // without keys there is nothing to load: the maps only have to be well formed
+    const long long rows = tk > 0 ? tk : 1;
+    bool fine = rows_map(&m.q, q_nope, p->d_nope, (int)H, tq, sq) && rows_map(&m.k, k_nope, p->d_nope, (int)KH, rows, sk) &&
+                rows_map(&m.v, v, p->d_v, (int)KH, rows, sv);
+    if (fine && p->d_rope > 0) {
+        fine = rows_map(&m.qr, q_rope, p->d_rope, (int)H, tq, sqr);
+        const cuuint64_t dims[2] = {(cuuint64_t)p->d_rope, (cuuint64_t)rows};
+        const cuuint64_t bytes[1] = {(cuuint64_t)skr[0] * 2};
+        const cuuint32_t box[2] = {64, kTile};
+        fine = fine && encode_tiled(&m.kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(k_rope), dims, bytes,
+                                    box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+    } else {
+        m.qr = m.q;
+        m.kr = m.k;
+    }
+    if (!fine)
+        return KVATTN_ERR_UNSUPPORTED;
+
+    char *ws = static_cast<char *>(workspace);
+    ragged::PlanArgs pa{};
+    pa.batch = p->batch;
+    pa.rows_per_tile = kItemRows;
+    pa.max_q = (int)tq;
+    pa.max_kv = (int)tk;
+    pa.capacity = (int)ragged::tile_capacity(tq, p->batch, kItemRows);
+    pa.causal = p->causal;
+    pa.q_start = q_start;
+    pa.kv_start = kv_start;
+    pa.header = reinterpret_cast<int32_t *>(ws);
+    pa.tiles = reinterpret_cast<ragged::Tile *>(ws + ragged::kPlanHeader);
+    pa.err = device_error;
+    c.stream = static_cast<cudaStream_t>(stream);
+    if (ragged::launch_plan(pa, c.stream) != cudaSuccess)
+        return KVATTN_ERR_CUDA;
+    PrefillArgs &a = c.args;
+    a.header = pa.header;
+    a.tiles = pa.tiles;
+    a.out = out;
+    a.lse = lse;
+    a.err = device_error;
+    a.heads = (int)H;
+    a.heads_per_kv = (int)(H / KH);
+    a.d_v = p->d_v;
+    a.out_fp32 = p->out_dtype == KVATTN_OUT_FP32;
+    a.causal = p->causal;
+    a.out_token_stride = so[0];
+    a.out_head_stride = so[1];
+    a.scale_log2 = sm_scale * 1.4426950408889634f;
+    c.most_items = pa.capacity * H;
+
+    const int nkn = (p->d_nope + 63) / 64, nvb = (p->d_v + 63) / 64;
+    const bool rope = p->d_rope > 0;
+    cudaError_t e;
+    if (nvb == 2)
+        e = nkn == 2 ? (rope ? launch<3, true, 2>(c) : launch<2, false, 2>(c))
+                     : (rope ? launch<2, true, 2>(c) : launch<1, false, 2>(c));
+    else
+        e = nkn == 2 ? (rope ? launch<3, true, 1>(c) : launch<2, false, 1>(c))
+                     : (rope ? launch<2, true, 1>(c) : launch<1, false, 1>(c));
+    return e == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
+}

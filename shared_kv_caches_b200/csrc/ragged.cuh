@@ -1,0 +1,91 @@
+// Pieces shared by the kernels over ragged batches (tables, expand, prefill):
+// sums over the requests and the lookup of the request an index falls in.
+#pragma once
+
+#include "kvattn_internal.cuh"
+#include "sm100.cuh"
+
+namespace kvattn {
+namespace ragged {
+
+constexpr int kThreads = 1024;           // threads of a block that sums over the requests
+constexpr int kMaxBatch = 16384;         // requests whose sums fit its shared memory
+
+// Exclusive sums over a block of kThreads threads; the total in `sum`.
+// sh: 32 values of shared memory.
+__device__ __forceinline__ long long block_scan(long long v, long long &sum, long long *sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long v0 = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += x;
+    }
+    __syncthreads();                      // sh may still be read by the scan before
+    if (lane == 31)
+        sh[warp] = v;
+    __syncthreads();
+    long long w = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o)
+            w += x;
+    }
+    sum = __shfl_sync(0xffffffffu, w, 31);
+    const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return v - v0 + (warp ? before : 0);
+}
+
+// The last index i in [0, n) with start[i] <= x (start ascending, start[0] <= x).
+__device__ __forceinline__ int find(const int32_t *start, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// One tile of a ragged batch, as the plan kernel lists them.
+struct Tile {
+    int32_t q0;       // first row of the tile
+    int32_t nq;       // rows of the tile
+    int32_t k0;       // first key row of the sequence
+    int32_t nk;       // keys of the sequence
+    int32_t lim0;     // keys that the tile's first row attends, before the clip to [0, nk]
+    int32_t seq;      // sequence
+    int32_t tok0;     // position of the first row in its sequence's rows
+    int32_t pad;
+};
+
+constexpr size_t kPlanHeader = 256;      // bytes in front of the tile list; its first int counts the tiles
+
+struct PlanArgs {
+    int batch, rows_per_tile;
+    int max_q, max_kv;
+    int capacity;                        // tiles the list has room for
+    int causal;
+    const int32_t *q_start;              // [batch + 1]
+    const int32_t *kv_start;             // [batch + 1]
+    int32_t *header;
+    Tile *tiles;
+    int32_t *err;
+};
+
+// Most tiles a batch can have: every sequence may end in one of its own.
+inline long long tile_capacity(long long rows, int batch, int rows_per_tile)
+{
+    return (rows + rows_per_tile - 1) / rows_per_tile + batch;
+}
+
+cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st);
+
+}  // namespace ragged
+}  // namespace kvattn

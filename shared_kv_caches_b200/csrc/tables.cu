@@ -1,0 +1,389 @@
+// A step's bookkeeping on the GPU: pages, positions and slots of the new
+// tokens of every request (kvattn_build_tables), and the write of their rows
+// into the paged cache by slot (kvattn_append_slots).
+//
+// build_tables.  With c_b cached and n_b new tokens of request b, request b
+// holds ceil(c_b / 64) pages and needs d_b = ceil((c_b + n_b) / 64) -
+// ceil(c_b / 64) more.  Three exclusive prefix sums over the requests (new
+// tokens, pages, context) give every chunk's start and every request's first
+// place in the free list; after them each token and each new page is a lookup
+// of its own:
+//   pos(t)  = c_b + t - q_start_b
+//   page(i) = i-th entry from the top of the free list for the request's new
+//             pages, the table's entry for the page it already holds
+// The whole call is one launch of one thread-block cluster: every CTA repeats
+// the sums (a few thousand integers) and takes a share of the tokens and
+// pages, and the lengths and the free count are written after a cluster
+// barrier, when every CTA has read them, so they may be updated in place (a
+// captured decode step advances by itself on each replay).
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "ragged.cuh"
+
+namespace kvattn {
+
+namespace {
+
+bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int kTableThreads = ragged::kThreads;
+constexpr int kTableMaxCtas = 8;           // the portable cluster size
+constexpr int kTokensPerCta = 4096;
+
+struct TableArgs {
+    int batch, mpps, num_pages, max_tokens;
+    const int32_t *cached, *fresh, *free_pages, *free_count;
+    int32_t *table, *seq_lens, *free_left, *q_start, *kv_start, *pos, *slots, *err;
+};
+
+__device__ __forceinline__ int pages_of(long long n) { return (int)((n + kPage - 1) / kPage); }
+
+__global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const TableArgs a)
+{
+    extern __shared__ int32_t sh_i[];
+    __shared__ long long sh_scan[32];
+    __shared__ int sh_taken;
+    int32_t *tok = sh_i;                            // [B + 1] first token of each chunk (at most max_tokens)
+    int32_t *pgs = sh_i + a.batch + 1;              // [B + 1] new pages of the requests before
+    int32_t *cch = sh_i + 2 * (a.batch + 1);        // [B] cached tokens, or -1 - cached where the request gets nothing
+    const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
+    const long long capacity = (long long)a.mpps * kPage;
+    const int raw_free = *a.free_count;
+    const int nfree = min(max(raw_free, 0), a.num_pages);
+    int bits = raw_free == nfree ? 0 : KVATTN_DEVERR_BAD_LENGTH;
+
+    const int per = (a.batch + kTableThreads - 1) / kTableThreads;
+    const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    // what request b asks for: its token count, and its pages if the lengths can be served at all
+    auto request = [&](int b, int &c, int &n, int &pages) -> bool {
+        c = a.cached[b];
+        n = a.fresh[b];
+        pages = 0;
+        if (c < 0 || n < 0) {
+            bits |= KVATTN_DEVERR_BAD_LENGTH;
+            c = max(c, 0);
+            n = max(n, 0);
+            return false;
+        }
+        if ((long long)c + n > capacity) {
+            bits |= KVATTN_DEVERR_SEQ_TOO_LONG;
+            return false;
+        }
+        pages = pages_of((long long)c + n) - pages_of(c);
+        return true;
+    };
+    long long ntok = 0, npg = 0, tok_total, pg_total;
+    for (int b = b0; b < b1; ++b) {
+        int c, n, pages;
+        request(b, c, n, pages);
+        ntok += n;
+        npg += pages;
+    }
+    ntok = ragged::block_scan(ntok, tok_total, sh_scan);
+    npg = ragged::block_scan(npg, pg_total, sh_scan);
+    long long ctx = 0, ctx_total;
+    int taken = 0;
+    {
+        long long t = ntok, p = npg;
+        for (int b = b0; b < b1; ++b) {
+            int c, n, pages;
+            bool ok = request(b, c, n, pages);
+            tok[b] = (int)min(t, (long long)a.max_tokens);
+            pgs[b] = (int)min(p, (long long)a.num_pages);
+            t += n;
+            p += pages;
+            if (n > 0 && t > a.max_tokens) {
+                bits |= KVATTN_DEVERR_TOO_MANY_TOKENS;
+                ok = false;
+            }
+            if (pages > 0 && p > nfree) {
+                bits |= KVATTN_DEVERR_POOL_EXHAUSTED;
+                ok = false;
+            }
+            cch[b] = ok ? c : -1 - c;
+            ctx += ok ? (long long)c + n : c;
+            // the requests that get pages are the first ones that ask for any
+            // (both sums only grow), so the list's top `taken` entries go
+            if (ok && pages > 0)
+                taken = (int)p;
+        }
+    }
+    const int total = (int)min(tok_total, (long long)a.max_tokens);
+    if (tid == 0) {
+        tok[a.batch] = total;
+        pgs[a.batch] = (int)min(pg_total, (long long)a.num_pages);
+        sh_taken = 0;
+    }
+    ctx = ragged::block_scan(ctx, ctx_total, sh_scan);
+    if (taken > 0)
+        atomicMax(&sh_taken, taken);
+    if (rank == 0 && bits && a.err)
+        atomicOr(a.err, bits);
+    // every CTA has read the lengths and the free count
+    cluster_sync_all();
+    taken = sh_taken;
+
+    if (rank == 0) {
+        for (int b = b0; b < b1; ++b) {
+            const int c = cch[b], n = max(a.fresh[b], 0);
+            const int len = c >= 0 ? c + n : -1 - c;
+            a.seq_lens[b] = len;
+            a.q_start[b] = tok[b];
+            if (a.kv_start)
+                a.kv_start[b] = (int)min(ctx, (long long)INT32_MAX);
+            ctx += len;
+        }
+        if (tid == 0) {
+            a.q_start[a.batch] = total;
+            if (a.kv_start)
+                a.kv_start[a.batch] = (int)min(ctx_total, (long long)INT32_MAX);
+            *a.free_left = nfree - taken;
+        }
+    }
+    bits = 0;
+    for (int i = rank * kTableThreads + tid; i < taken; i += ctas * kTableThreads) {
+        const int b = ragged::find(pgs, a.batch, i);
+        const int page = a.free_pages[nfree - 1 - i];
+        if (page < 0 || page >= a.num_pages)
+            bits = KVATTN_DEVERR_PAGE_OUT_OF_RANGE;
+        a.table[(long long)b * a.mpps + pages_of(cch[b]) + i - pgs[b]] = page;
+    }
+#pragma unroll 4
+    for (int t = rank * kTableThreads + tid; t < total; t += ctas * kTableThreads) {
+        const int b = ragged::find(tok, a.batch, t);
+        const int c = cch[b];
+        const long long p = (long long)(c >= 0 ? c : -1 - c) + t - tok[b];
+        int slot = -1;
+        if (c >= 0) {
+            const int pi = (int)(p / kPage), held = pages_of(c);
+            const int page = pi < held ? a.table[(long long)b * a.mpps + pi]
+                                       : a.free_pages[nfree - 1 - (pgs[b] + pi - held)];
+            if (page < 0 || page >= a.num_pages)
+                bits = KVATTN_DEVERR_PAGE_OUT_OF_RANGE;
+            else
+                slot = page * kPage + (int)(p % kPage);
+        }
+        a.pos[t] = (int)min(p, (long long)INT32_MAX);
+        a.slots[t] = slot;
+    }
+    for (int t = total + rank * kTableThreads + tid; t < a.max_tokens; t += ctas * kTableThreads) {
+        a.pos[t] = 0;
+        a.slots[t] = -1;
+    }
+    if (bits && a.err)
+        atomicOr(a.err, bits);
+}
+
+// ------------------------------------------------------- append by slot
+
+constexpr int kAppendThreads = 256;
+
+struct SlotAppendArgs {
+    const __nv_bfloat16 *src;     // [tokens][planes][row]
+    const int32_t *pos;           // [tokens]; read only where rows are turned
+    const int32_t *slots;         // [tokens]
+    void *cache;
+    int32_t *err;                 // may be null
+    int tokens, planes, row;
+    int copy;                     // leading elements of plane 0 taken as they are
+    int rot_width, rot_count;     // RoPE over rot_count slices of rot_width after `copy`
+    long long num_slots;
+    double log2_base;
+    float k_scale, v_scale;       // fp8: what a stored value is multiplied by when it is read
+};
+
+__device__ __forceinline__ double rope_rate(int i, int width, double log2_base)
+{
+    return exp2(-2.0 * (double)i / (double)width * log2_base);
+}
+
+// Two values as e4m3 bytes, nearest even, saturated at +-448.
+__device__ __forceinline__ uint16_t e4m3_pair(float x, float y)
+{
+    return (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Eight bf16 values divided by scale, as e4m3 bytes.
+__device__ __forceinline__ uint2 e4m3_oct(uint4 v, float scale)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = e4m3_pair(__uint_as_float(w[i] << 16) / scale, __uint_as_float(w[i] & 0xffff0000u) / scale);
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+
+// One warp per token: 16-byte copies of what is stored as it is; a turned
+// pair belongs to one lane, which forms its angle once for the token and turns
+// the pair of every slice (every K head) with it.  The angle and the turn are
+// in double precision with one rounding to the stored type, as kvattn_rope's;
+// a lane's first two rates (all it has for slices up to 128 wide) stay in
+// registers over its tokens.
+template <bool FP8>
+__global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const SlotAppendArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (kAppendThreads / 32);
+    const int half = a.rot_width / 2;
+    double rate0 = 0.0, rate1 = 0.0;
+    if (a.rot_count > 0) {
+        rate0 = rope_rate(lane, a.rot_width, a.log2_base);
+        rate1 = rope_rate(lane + 32, a.rot_width, a.log2_base);
+    }
+    for (int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < a.tokens; t += warps) {
+        const int slot = a.slots[t];
+        if (slot < 0 || slot >= a.num_slots) {
+            if (slot != -1 && lane == 0 && a.err)
+                atomicOr(a.err, KVATTN_DEVERR_PAGE_OUT_OF_RANGE);
+            continue;
+        }
+        const long long page = slot / kPage;
+        const int off = slot % kPage;
+        for (int pl = 0; pl < a.planes; ++pl) {
+            const __nv_bfloat16 *src = a.src + ((long long)t * a.planes + pl) * a.row;
+            const long long at = ((page * a.planes + pl) * kPage + off) * (long long)a.row;
+            const bool turn = a.rot_count > 0 && pl == 0;
+            const int copy = turn ? a.copy : a.row;
+            const float scale = pl == 0 ? a.k_scale : a.v_scale;
+#pragma unroll 4
+            for (int i = lane; i < copy / 8; i += 32) {
+                const uint4 v = reinterpret_cast<const uint4 *>(src)[i];
+                if constexpr (FP8)
+                    reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache) + at)[i] = e4m3_oct(v, scale);
+                else
+                    reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + at)[i] = v;
+            }
+            if (!turn)
+                continue;
+            const double p = (double)a.pos[t];
+            for (int i = lane; i < half; i += 32) {
+                const double rate = i == lane ? rate0 : i == lane + 32 ? rate1 : rope_rate(i, a.rot_width, a.log2_base);
+                double s, c;
+                sincos(p * rate, &s, &c);
+#pragma unroll 4
+                for (int n = 0; n < a.rot_count; ++n) {
+                    const int e = copy + n * a.rot_width + 2 * i;
+                    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(src + e);
+                    const double x = (double)__bfloat162float(v.x), y = (double)__bfloat162float(v.y);
+                    const double rx = x * c - y * s, ry = x * s + y * c;
+                    if constexpr (FP8) {
+                        *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.cache) + at + e) =
+                            e4m3_pair((float)(rx / (double)scale), (float)(ry / (double)scale));
+                    } else {
+                        __nv_bfloat162 r;
+                        r.x = __double2bfloat16(rx);
+                        r.y = __double2bfloat16(ry);
+                        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.cache) + at + e) = r;
+                    }
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+}  // namespace kvattn
+
+using namespace kvattn;
+
+extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int32_t num_pages, int32_t max_tokens,
+                                   const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
+                                   const int32_t *free_count, int32_t *block_table, int32_t *seq_lens,
+                                   int32_t *free_left, int32_t *q_start, int32_t *kv_start, int32_t *pos,
+                                   int32_t *slots, int32_t *device_error, void *stream)
+{
+    if (batch < 1 || max_pages_per_seq < 1 || num_pages < 1 || max_tokens < 0)
+        return KVATTN_ERR_INVALID_ARG;
+    if (!cached_lens || !new_lens || !free_pages || !free_count || !block_table || !seq_lens || !free_left ||
+        !q_start || (max_tokens > 0 && (!pos || !slots)))
+        return KVATTN_ERR_INVALID_ARG;
+    if (batch > ragged::kMaxBatch || num_pages > INT32_MAX / kPage)
+        return KVATTN_ERR_UNSUPPORTED;
+    for (const void *p : {static_cast<const void *>(cached_lens), static_cast<const void *>(new_lens),
+                          static_cast<const void *>(free_pages), static_cast<const void *>(free_count),
+                          static_cast<const void *>(block_table), static_cast<const void *>(seq_lens),
+                          static_cast<const void *>(free_left), static_cast<const void *>(q_start),
+                          static_cast<const void *>(kv_start), static_cast<const void *>(pos),
+                          static_cast<const void *>(slots), static_cast<const void *>(device_error)})
+        if (!is_aligned(p, 4))
+            return KVATTN_ERR_MISALIGNED;
+    TableArgs a{batch, max_pages_per_seq, num_pages, max_tokens, cached_lens, new_lens, free_pages, free_count,
+                block_table, seq_lens, free_left, q_start, kv_start, pos, slots, device_error};
+    int ctas = (max_tokens + kTokensPerCta - 1) / kTokensPerCta;
+    ctas = ctas < 1 ? 1 : ctas > kTableMaxCtas ? kTableMaxCtas : ctas;
+    const size_t smem = (3 * (size_t)batch + 2) * sizeof(int32_t);
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)smem) != cudaSuccess)
+        return KVATTN_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kTableThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, build_tables_kernel, (const TableArgs)a) == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
+}
+
+extern "C" int kvattn_append_slots(int32_t variant, const kvattn_params *p, const void *new_kv, int32_t num_tokens,
+                                   const int32_t *pos, const int32_t *slots, void *kv_cache, float rope_base,
+                                   int32_t *device_error, void *stream)
+{
+    Problem pr;
+    const int st = validate_params(variant, p, &pr);
+    if (st)
+        return st;
+    if (num_tokens < 0 || !new_kv || !slots || !kv_cache)
+        return KVATTN_ERR_INVALID_ARG;
+    if (!(rope_base == 0.f || (rope_base > 1.f && isfinite(rope_base))))
+        return KVATTN_ERR_INVALID_ARG;
+    if (rope_base > 0.f && !pos)
+        return KVATTN_ERR_INVALID_ARG;
+    const bool tied = !pr.latent && pr.kv_planes == 1;
+    if (tied && rope_base != 0.f)
+        return KVATTN_ERR_INVALID_ARG;      // the row is the value too (as in kvattn_append_kv)
+    if (pr.num_pages > INT32_MAX / kPage)
+        return KVATTN_ERR_UNSUPPORTED;
+    if (!is_aligned(new_kv, 16) || !is_aligned(kv_cache, 16) || !is_aligned(pos, 4) || !is_aligned(slots, 4) ||
+        !is_aligned(device_error, 4))
+        return KVATTN_ERR_MISALIGNED;
+    if (num_tokens == 0)
+        return KVATTN_OK;
+    const bool fp8 = p->cache_dtype == KVATTN_CACHE_FP8_E4M3;
+    SlotAppendArgs a{};
+    a.src = static_cast<const __nv_bfloat16 *>(new_kv);
+    a.pos = pos;
+    a.slots = slots;
+    a.cache = kv_cache;
+    a.err = device_error;
+    a.tokens = num_tokens;
+    a.row = pr.row;
+    a.planes = pr.latent || tied ? 1 : 2;
+    a.num_slots = (long long)pr.num_pages * kPage;
+    a.log2_base = rope_base > 0.f ? log2((double)rope_base) : 0.0;
+    a.k_scale = fp8 ? p->k_scale : 1.f;
+    a.v_scale = fp8 ? p->v_scale : 1.f;
+    if (rope_base > 0.f) {
+        a.copy = pr.latent ? pr.NU * pr.dn : 0;
+        a.rot_width = pr.latent ? pr.dr : pr.dn;
+        a.rot_count = pr.latent ? (pr.dr > 0 ? 1 : 0) : pr.NU;
+    }
+    const int per = kAppendThreads / 32;
+    const long long want = ((long long)num_tokens + per - 1) / per;
+    const long long most = 8LL * sm_count();      // eight resident blocks an SM: every SM full, rates kept over tokens
+    const int grid = (int)(want < most ? want : most);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (fp8)
+        append_slots_kernel<true><<<grid, kAppendThreads, 0, s>>>(a);
+    else
+        append_slots_kernel<false><<<grid, kAppendThreads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
+}

@@ -1,0 +1,638 @@
+"""The prompt side on the GPU (kvattn_build_tables, kvattn_append_slots,
+kvattn_expand_kv, kvattn_prefill) against the fp64 reference in
+oracle/prompt.py.
+
+Tolerances, from the arithmetic (a rounding to bf16 is off by at most 2^-8 of
+the value, to e4m3 by 2^-4, in fp32 by 2^-24):
+* tables: whole numbers, equal.
+* append: copied parts equal; a turned pair is formed in double precision and
+  rounded once, as the reference's is, so at most one bf16 step apart (a
+  double's rounding next to a tie) and hardly ever; e4m3 likewise.
+* expand: products of bf16 are exact in fp32, d_c <= 512 of them are added in
+  fp32: 1e-5 of sum |c w| covers the sums (512 * 2^-24 = 3e-5 if every rounding
+  went one way; they do not over more than a third), and one rounding: 2^-8 |y|.
+* prefill: a score is a sum of at most 192 exact products in fp32, off by at
+  most 192 * 2^-24 = 1.2e-5 of scale * sum |q k| (`reach`), and the exponent's
+  fma, 2^x (2 ulp) and the sums add less than 1e-5 + 2^-23 |m| with |m| <= reach;
+  delta = 1.5e-5 * reach + 1e-5.  A weight is off by 2 delta (itself and the
+  denominator) and rounded to bf16 for P.V: |out| off by (2^-8 + 2 delta) sum p
+  |v|, and its own rounding 2^-8 |out| when it is stored in bf16.  lse is off by
+  delta + 2^-22 |lse|.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import prompt
+from shared_kv_caches_b200 import kvattn as K
+from shared_kv_caches_b200 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+BF16 = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from shared_kv_caches_b200 import build
+    build.build()
+    return torch.device("cuda:0")
+
+
+def bits(rng, *shape, scale=1.0):
+    return W.f32_to_bf16_bits((rng.standard_normal(shape) * scale).astype(np.float32))
+
+
+def f64(b):
+    return W.bf16_bits_to_f32(np.asarray(b)).astype(np.float64)
+
+
+def up(b, dev):
+    from shared_kv_caches_b200.device import bf16_tensor
+    return bf16_tensor(b, dev)
+
+
+def i32(x, dev):
+    import torch
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)
+
+
+def down(t):
+    return t.detach().double().cpu().numpy()
+
+
+def word(dev):
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def starts(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+# ------------------------------------------------------------------ tables
+
+def table_case(rng, cached, new, mpps=None, spare=3, shrink=0):
+    cached, new = np.asarray(cached), np.asarray(new)
+    held = -(-np.maximum(cached, 0) // 64)
+    need = -(-np.maximum(cached + new, 0) // 64)
+    mpps = int(max(need.max(), 1)) if mpps is None else mpps
+    num_pages = int(need.sum()) + spare
+    perm = rng.permutation(num_pages)
+    table = np.full((len(cached), mpps), -7, dtype=np.int64)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :min(h, mpps)] = perm[at:at + min(h, mpps)]
+        at += h
+    free = perm[at:]
+    count = max(len(free) - shrink, 0)
+    return table, np.concatenate([free, np.full(at, -1)])[:num_pages], count, num_pages
+
+
+def run_tables(dev, cached, new, table, free, count, max_tokens, **kw):
+    err = word(dev)
+    r = K.build_tables_tensors(i32(cached, dev), i32(new, dev), i32(free, dev), i32([count], dev), i32(table, dev),
+                               max_tokens, device_error=err, **kw)
+    return {k: v.cpu().numpy().astype(np.int64) for k, v in r.items()} | {"err": int(err.item())}
+
+
+def same_tables(got, ref):
+    for k in ref:
+        np.testing.assert_array_equal(got[k], ref[k], err_msg=k)
+
+
+@pytest.mark.parametrize("cached,new", [
+    ([0], [1]), ([63], [1]), ([64], [1]), ([0], [0]), ([5], [200]), ([1, 0, 64, 63, 128], [1, 1, 1, 1, 1]),
+    ([0, 10, 0, 64], [0, 0, 130, 64]), ([0] * 40, list(range(40))),
+])
+def test_tables_small(dev, cached, new):
+    rng = np.random.default_rng(1)
+    table, free, count, pages = table_case(rng, cached, new)
+    m = sum(new) + 5
+    same_tables(run_tables(dev, cached, new, table, free, count, m),
+                prompt.build_tables(cached, new, free, count, table, m, pages))
+
+
+@pytest.mark.parametrize("batch,hi,past", [(1, 40000, 0), (7, 9000, 3000), (1025, 3, 700), (3000, 64, 0), (16384, 1, 129)])
+def test_tables_large(dev, batch, hi, past):
+    rng = np.random.default_rng(batch)
+    cached, new = rng.integers(0, past + 1, batch), rng.integers(0, hi + 1, batch)
+    table, free, count, pages = table_case(rng, cached, new)
+    m = int(new.sum())
+    same_tables(run_tables(dev, cached, new, table, free, count, m),
+                prompt.build_tables(cached, new, free, count, table, m, pages))
+
+
+@pytest.mark.parametrize("shrink", [1, 4, 100])
+def test_tables_pool_runs_out(dev, shrink):
+    rng = np.random.default_rng(shrink)
+    cached, new = rng.integers(0, 200, 30), rng.integers(0, 300, 30)
+    table, free, count, pages = table_case(rng, cached, new, shrink=shrink, spare=0)
+    m = int(new.sum()) + 3
+    ref = prompt.build_tables(cached, new, free, count, table, m, pages)
+    assert ref["err"] == prompt.ERR_POOL
+    same_tables(run_tables(dev, cached, new, table, free, count, m), ref)
+
+
+@pytest.mark.parametrize("case", ["tokens", "long", "negative", "bad_free", "bad_held", "no_free", "count"])
+def test_tables_bad_requests_get_nothing(dev, case):
+    rng = np.random.default_rng(5)
+    cached, new = np.array([10, 64, 0, 130, 7]), np.array([3, 100, 64, 0, 70])
+    table, free, count, pages = table_case(rng, cached, new)
+    m, want = int(new.sum()), {"tokens": prompt.ERR_TOKENS, "long": prompt.ERR_LONG, "negative": prompt.ERR_LENGTH,
+                               "bad_free": prompt.ERR_PAGE, "bad_held": prompt.ERR_PAGE, "no_free": prompt.ERR_POOL,
+                               "count": prompt.ERR_LENGTH}[case]
+    if case == "tokens":
+        m = 150
+    elif case == "long":
+        cached[1] = 64 * table.shape[1]
+    elif case == "negative":
+        new[1], cached[3] = -5, -1
+    elif case == "bad_free":
+        free[count - 2] = pages
+    elif case == "bad_held":
+        table[0, 0] = -1
+    elif case == "no_free":
+        count = 0
+    else:
+        count = pages + 9
+        free[:] = rng.permutation(pages)
+    ref = prompt.build_tables(cached, new, free, count, table, m, pages)
+    assert ref["err"] == want
+    same_tables(run_tables(dev, cached, new, table, free, count, m), ref)
+
+
+def test_tables_in_place_step_replays_in_a_graph(dev):
+    """Lengths and free list updated in place: each replay is one more step."""
+    import torch
+    cached, new = np.array([62, 0, 127]), np.array([1, 1, 2])
+    rng = np.random.default_rng(8)
+    table, free, count, pages = table_case(rng, cached, new + 20, mpps=8)
+    lens, cnt, tab, one, pool = i32(cached, dev), i32([count], dev), i32(table, dev), i32(new, dev), i32(free, dev)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        r = K.build_tables_tensors(lens, one, pool, cnt, tab, 6, inplace=True)
+    ref_c, ref_t, ref_n = cached, table, count
+    for _ in range(6):
+        g.replay()
+        torch.cuda.synchronize()
+        ref = prompt.build_tables(ref_c, new, free, ref_n, ref_t, 6, pages)
+        ref.pop("err")
+        same_tables({k: v.cpu().numpy() for k, v in r.items()}, ref)
+        ref_c, ref_t, ref_n = ref["seq_lens"], ref["block_table"], int(ref["free_left"][0])
+
+
+# ------------------------------------------------------------------ append
+
+def turned_close(got, ref, step):
+    """Equal but for values next to a tie, which may land one step away."""
+    off = np.abs(got - ref) > 0
+    assert np.all(np.abs(got - ref)[off] <= 2 * step * np.abs(ref)[off] + 2.0 ** -130)
+    assert off.mean() < 1e-3
+
+
+def bf16_round(x):
+    m, e = np.frexp(np.asarray(x, dtype=np.float64))
+    return np.ldexp(np.rint(m * 256.0), e - 8)
+
+
+@pytest.mark.parametrize("variant,heads,kv,dn,dr", [("mla", 128, 1, 512, 64), ("gla", 8, 4, 128, 32), ("mlra", 4, 2, 64, 16),
+                                                    ("mla", 4, 1, 72, 0), ("mla", 4, 1, 64, 128)])
+@pytest.mark.parametrize("base", [0.0, W.ROPE_BASE])
+def test_append_latent_rows(dev, variant, heads, kv, dn, dr, base):
+    import torch
+    rng = np.random.default_rng(3)
+    row, pages, n = kv * dn + dr, 9, 203
+    cache, rows = bits(rng, pages, 64, row), bits(rng, n, row)
+    slots = rng.permutation(pages * 64)[:n].astype(np.int32)
+    slots[[0, 50]] = -1
+    pos = rng.integers(0, 1 << 20, n)
+    pos[3], pos[4] = 0, -5
+    p = K.make_params(1, heads, kv, dn, dr, pages, pages, 0)
+    t, err = up(cache, dev), word(dev)
+    K.append_slots_tensor(K.VARIANTS[variant], p, up(rows, dev), i32(pos, dev), i32(slots, dev), t, base, err)
+    ref = prompt.append_rows(f64(cache), f64(rows), pos, slots, [(kv * dn, dr)] if dr else [], base)
+    got = down(t)
+    assert int(err.item()) == 0
+    np.testing.assert_array_equal(got[..., :kv * dn], ref[..., :kv * dn])
+    if base and dr:
+        turned_close(got[..., kv * dn:], bf16_round(ref[..., kv * dn:]), BF16)
+    else:
+        np.testing.assert_array_equal(got, ref)
+
+
+@pytest.mark.parametrize("variant,kv,d", [("gqa", 8, 128), ("gqa", 2, 64), ("mqa", 1, 256), ("gqa", 3, 512), ("gta", 4, 128)])
+def test_append_head_rows(dev, variant, kv, d):
+    rng = np.random.default_rng(4)
+    planes, base = (1, 0.0) if variant == "gta" else (2, W.ROPE_BASE)
+    pages, n = 5, 150
+    cache, rows = bits(rng, pages, planes, 64, kv * d), bits(rng, n, planes, kv * d)
+    slots, pos = rng.permutation(pages * 64)[:n], rng.integers(0, 40000, n)
+    p = K.make_params(1, 2 * kv, kv, d, 0, pages, pages, 0)
+    t = up(cache, dev)
+    K.append_slots_tensor(K.VARIANTS[variant], p, up(rows, dev), i32(pos, dev), i32(slots, dev), t, base)
+    got = down(t)
+    for pl in range(planes):
+        turn = base if pl == 0 else 0.0
+        ref = prompt.append_rows(f64(cache[:, pl]), f64(rows[:, pl]), pos, slots, [(h * d, d) for h in range(kv)], turn)
+        if turn:
+            turned_close(got[:, pl], bf16_round(ref), BF16)
+        else:
+            np.testing.assert_array_equal(got[:, pl], ref)
+
+
+@pytest.mark.parametrize("base", [0.0, W.ROPE_BASE])
+def test_append_quantises_into_the_fp8_cache(dev, base):
+    import torch
+    from oracle import oracle
+    rng = np.random.default_rng(6)
+    kv, d, pages, n = 8, 128, 4, 130
+    cache = rng.integers(0, 256, (pages, 2, 64, kv, d)).astype(np.uint8)
+    rows = bits(rng, n, 2, kv * d, scale=3.0)
+    rows[5, 1, :4] = W.f32_to_bf16_bits(np.array([1e5, -1e5, 0.0, 2.0 ** -12], np.float32))
+    rows[6, 1, 0] = W.BF16_NAN
+    slots, pos = rng.permutation(pages * 64)[:n], rng.integers(0, 40000, n)
+    p = K.make_params(1, 32, kv, d, 0, pages, pages, 0, cache_dtype=K.KVATTN_CACHE_FP8_E4M3, k_scale=0.37, v_scale=1.7)
+    t = torch.from_numpy(cache).to(dev)
+    K.append_slots_tensor(K.KVATTN_GQA, p, up(rows, dev), i32(pos, dev), i32(slots, dev), t, base)
+    got = t.cpu().numpy()
+    ks, vs = float(np.float32(0.37)), float(np.float32(1.7))
+    flat = got.transpose(0, 2, 1, 3, 4).reshape(pages * 64, 2, kv * d)
+    old = cache.transpose(0, 2, 1, 3, 4).reshape(pages * 64, 2, kv * d)
+    rest = np.setdiff1d(np.arange(pages * 64), slots)
+    np.testing.assert_array_equal(flat[rest], old[rest])
+    k = prompt.append_rows(np.zeros((pages, 64, kv * d)), f64(rows[:, 0]), pos, slots, [(h * d, d) for h in range(kv)], base)
+    k = k.reshape(pages * 64, kv * d)[slots] / ks
+    v = (f64(rows[:, 1]).astype(np.float32) / np.float32(vs)).astype(np.float64)
+    for have, want in ((flat[slots, 0], k), (flat[slots, 1], v)):
+        code = W.f32_to_e4m3_bits(want)
+        # next to a tie the two may round apart: neighbouring codes
+        apart = np.abs(have.astype(int) - code.astype(int))
+        assert apart.max() <= 1 and (apart > 0).mean() < 1e-3
+    assert oracle.e4m3_value(flat[slots[5], 1, 0]) == 448.0 and flat[slots[6], 1, 0] & 0x7F == 0x7F
+
+
+def test_append_bad_slots_are_skipped(dev):
+    rng = np.random.default_rng(7)
+    cache, rows = bits(rng, 2, 64, 72), bits(rng, 4, 72)
+    p = K.make_params(1, 4, 1, 64, 8, 2, 2, 0)
+    t, err = up(cache, dev), word(dev)
+    K.append_slots_tensor(K.KVATTN_MLA, p, up(rows, dev), i32([1, 2, 3, 4], dev), i32([128, -2, 5, -1], dev), t, 0.0, err)
+    ref = f64(cache)
+    ref[0, 5] = f64(rows[2])
+    np.testing.assert_array_equal(down(t), ref)
+    assert int(err.item()) == K.KVATTN_DEVERR_PAGE_OUT_OF_RANGE
+
+
+# ------------------------------------------------------------------ expand
+
+def expand_case(rng, dev, H, G, dc, dr, dk, dv, lens, paged=True, extra=0):
+    need = [-(-n // 64) for n in lens]
+    mpps = max(need + [1])
+    pages = (sum(need) + 2) if paged else mpps * len(lens)
+    cache = bits(rng, pages, 64, G * dc + dr)
+    if paged:
+        perm, at = rng.permutation(pages), 0
+        table = np.full((len(lens), mpps), pages + 5, dtype=np.int32)
+        for b, n in enumerate(need):
+            table[b, :n] = perm[at:at + n]
+            at += n
+    else:
+        table = None
+    for b, n in enumerate(lens):       # slots past the length hold anything
+        if n % 64:
+            pg = table[b, n // 64] if paged else b * mpps + n // 64
+            cache[pg, n % 64:] = W.BF16_NAN
+    uk, uv = bits(rng, H, dk, dc, scale=dc ** -0.5), bits(rng, H, dc, dv, scale=dc ** -0.5)
+    p = K.make_params(len(lens), H, G, dc, dr, mpps, pages, 0)
+    return cache, table, uk, uv, p, mpps
+
+
+def check_expand(got, cache, table, uk, uv, groups, lens, mpps):
+    st = starts(lens)
+    for b, n in enumerate(lens):
+        rows = prompt.gather(f64(cache), table, b, n, mpps)
+        k, v, ka, va = prompt.expand(rows, f64(uk), f64(uv), groups)
+        gk, gv = down(got["k"][:, st[b]:st[b + 1]]), down(got["v"][:, st[b]:st[b + 1]])
+        assert np.all(np.abs(gk - k) <= BF16 * np.abs(k) + 1e-5 * ka)
+        assert np.all(np.abs(gv - v) <= BF16 * np.abs(v) + 1e-5 * va)
+        if got["k_rope"] is not None:
+            np.testing.assert_array_equal(down(got["k_rope"][st[b]:st[b + 1]]), rows[:, groups * uk.shape[2]:])
+
+
+@pytest.mark.parametrize("H,G,dc,dr,dk,dv,lens,paged", [
+    (4, 1, 512, 64, 128, 128, [1, 0, 63, 64, 65, 127, 128, 129, 300], True),
+    (8, 2, 256, 64, 128, 128, [200, 1], True),
+    (6, 2, 128, 32, 64, 128, [130, 0, 70], True),
+    (3, 1, 64, 16, 40, 72, [100, 129], False),
+    (2, 1, 64, 0, 8, 8, [257], True),
+    (130, 1, 64, 64, 128, 64, [64, 64], True),
+])
+def test_expand_matches_reference(dev, H, G, dc, dr, dk, dv, lens, paged):
+    rng = np.random.default_rng(H + dc)
+    cache, table, uk, uv, p, mpps = expand_case(rng, dev, H, G, dc, dr, dk, dv, lens, paged)
+    err = word(dev)
+    got = K.expand_kv_tensors(K.KVATTN_MLA if G == 1 else K.KVATTN_GLA, p, up(cache, dev),
+                              None if table is None else i32(table, dev), i32(starts(lens), dev), up(uk, dev), up(uv, dev),
+                              sum(lens), err)
+    assert int(err.item()) == 0
+    check_expand(got, cache, table, uk, uv, G, lens, mpps)
+
+
+def test_expand_leaves_rows_past_the_last_sequence(dev):
+    import torch
+    rng = np.random.default_rng(2)
+    lens = [70, 130]
+    cache, table, uk, uv, p, mpps = expand_case(rng, dev, 2, 1, 64, 16, 64, 128, lens)
+    n = sum(lens) + 77
+    k = torch.full((2, n, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    v = torch.full((2, n, 128), 7.0, dtype=torch.bfloat16, device=dev)
+    kr = torch.full((n, 16), 7.0, dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, n), dtype=torch.uint8, device=dev)
+    c, t, s, a, b = up(cache, dev), i32(table, dev), i32(starts(lens), dev), up(uk, dev), up(uv, dev)
+    assert K.kvattn_expand_kv(K.KVATTN_MLA, p, c.data_ptr(), t.data_ptr(), s.data_ptr(), n, 64, 128, a.data_ptr(),
+                              b.data_ptr(), k.data_ptr(), v.data_ptr(), kr.data_ptr(), ws.data_ptr(), ws.numel(), None,
+                              torch.cuda.current_stream().cuda_stream) == 0
+    check_expand(dict(k=k, v=v, k_rope=kr), cache, table, uk, uv, 1, lens, mpps)
+    for x in (k[:, sum(lens):], v[:, sum(lens):], kr[sum(lens):]):
+        assert bool((x == 7.0).all())
+
+
+def test_expand_bad_page_gives_zeros_and_the_bit(dev):
+    rng = np.random.default_rng(9)
+    lens = [100, 200]
+    cache, table, uk, uv, p, mpps = expand_case(rng, dev, 3, 1, 64, 16, 64, 64, lens)
+    table[1, 2] = -3
+    err = word(dev)
+    got = K.expand_kv_tensors(K.KVATTN_MLA, p, up(cache, dev), i32(table, dev), i32(starts(lens), dev), up(uk, dev),
+                              up(uv, dev), sum(lens), err)
+    assert int(err.item()) == K.KVATTN_DEVERR_PAGE_OUT_OF_RANGE
+    for x in (got["k"][:, 228:292], got["v"][:, 228:292], got["k_rope"][228:292]):
+        assert bool((x == 0).all())
+    check_expand({k: v[..., :228, :] for k, v in got.items()}, cache, table, uk, uv, 1, [100, 128], mpps)
+
+
+# ----------------------------------------------------------------- prefill
+
+def prefill_case(rng, H, KH, dn, dr, dv, ql, kl, slack=9):
+    tq, tk = sum(ql) + slack, sum(kl) + slack
+    x = dict(q=bits(rng, tq, H, dn), k=bits(rng, KH, tk, dn), v=bits(rng, KH, tk, dv),
+             qr=bits(rng, tq, H, dr) if dr else None, kr=bits(rng, tk, dr) if dr else None)
+    for name in ("k", "v"):
+        x[name][:, sum(kl):] = W.BF16_NAN
+    if dr:
+        x["kr"][sum(kl):] = W.BF16_NAN
+    x["q"][sum(ql):] = W.BF16_NAN
+    return x
+
+
+def check_prefill(got, x, ql, kl, scale, causal, fp32=False, skip=()):
+    H, KH = x["q"].shape[1], x["k"].shape[0]
+    out, lse = down(got["out"]), down(got["lse"])
+    qs, ks = starts(ql), starts(kl)
+    for b in range(len(ql)):
+        if b in skip:
+            continue
+        a, e, c, d = qs[b], qs[b + 1], ks[b], ks[b + 1]
+        for h in range(H):
+            q, k = f64(x["q"][a:e, h]), f64(x["k"][h // (H // KH), c:d])
+            if x["qr"] is not None:
+                q = np.concatenate([q, f64(x["qr"][a:e, h])], 1)
+                k = np.concatenate([k, f64(x["kr"][c:d])], 1)
+            ro, rl, mass, reach = prompt.attention(q, k, f64(x["v"][h // (H // KH), c:d]), scale, causal)
+            delta = 1.5e-5 * reach + 1e-5
+            tol = (BF16 + 2 * delta)[:, None] * mass + (0 if fp32 else BF16) * np.abs(ro) + 1e-30
+            assert np.all(np.abs(out[a:e, h] - ro) <= tol), (b, h, np.abs(out[a:e, h] - ro).max())
+            none = np.isinf(rl)
+            np.testing.assert_array_equal(lse[a:e, h][none], rl[none])
+            assert np.all(np.abs(lse[a:e, h] - rl)[~none] <= (delta + 2.0 ** -22 * np.abs(rl))[~none]), (b, h)
+
+
+def call(dev, x, ql, kl, scale, causal, **kw):
+    t = {k: None if v is None else up(v, dev) for k, v in x.items()}
+    return K.prefill_tensors(t["q"], t["qr"], t["k"], t["kr"], t["v"], i32(starts(ql), dev), i32(starts(kl), dev), scale,
+                             causal=causal, **kw)
+
+
+LENS = [([1], [1]), ([1], [200]), ([127], [127]), ([128], [128]), ([129], [129]), ([256], [256]), ([257], [300]),
+        ([0, 3, 0, 130, 1], [5, 3, 0, 400, 64]), ([300, 2], [300, 1000]), ([2, 200], [0, 150])]
+
+
+@pytest.mark.parametrize("ql,kl", LENS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_lengths(dev, ql, kl, causal):
+    """Lengths around the tiles, cached prefixes, sequences without queries or keys, rows whose mask leaves nothing."""
+    rng = np.random.default_rng(sum(ql) + sum(kl))
+    x = prefill_case(rng, 2, 2, 128, 64, 128, ql, kl)
+    err = word(dev)
+    got = call(dev, x, ql, kl, 192 ** -0.5, causal, device_error=err)
+    assert int(err.item()) == 0
+    check_prefill(got, x, ql, kl, 192 ** -0.5, causal)
+
+
+@pytest.mark.parametrize("H,KH,dn,dr,dv", [(4, 1, 128, 0, 128), (8, 2, 64, 0, 64), (3, 3, 64, 16, 64), (2, 1, 64, 64, 128),
+                                           (2, 2, 128, 64, 64), (2, 2, 72, 8, 40), (9, 3, 8, 0, 8), (2, 2, 128, 32, 96),
+                                           (17, 17, 64, 0, 128)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_prefill_head_layouts(dev, H, KH, dn, dr, dv, fp32):
+    rng = np.random.default_rng(H * dn + dv)
+    ql, kl = [150, 1, 77], [150, 140, 300]
+    x = prefill_case(rng, H, KH, dn, dr, dv, ql, kl)
+    got = call(dev, x, ql, kl, (dn + dr) ** -0.5, True, out_fp32=fp32)
+    check_prefill(got, x, ql, kl, (dn + dr) ** -0.5, True, fp32)
+
+
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1.0])
+def test_prefill_scales(dev, scale):
+    """A negative scale, none (every key weighs the same), and scores far apart."""
+    rng = np.random.default_rng(11)
+    ql, kl = [140], [270]
+    x = prefill_case(rng, 2, 2, 128, 64, 128, ql, kl)
+    check_prefill(call(dev, x, ql, kl, scale, True), x, ql, kl, scale, True)
+
+
+def test_prefill_rising_maxima(dev):
+    """Scores that keep growing along the keys: the running maximum moves and outputs are rescaled in every tile."""
+    rng = np.random.default_rng(12)
+    ql, kl = [130], [900]
+    x = prefill_case(rng, 1, 1, 64, 0, 64, ql, kl)
+    ramp = np.linspace(0.0, 4.0, 900)[:, None]
+    x["k"][0, :900] = W.f32_to_bf16_bits((f64(x["k"][0, :900]) * 0.1 + ramp).astype(np.float32))
+    x["q"][:130, 0] = W.f32_to_bf16_bits((np.abs(f64(x["q"][:130, 0])) + 0.2).astype(np.float32))
+    check_prefill(call(dev, x, ql, kl, 0.5, False), x, ql, kl, 0.5, False)
+
+
+def test_prefill_strided_views(dev):
+    """Keys and values token by token, queries as slices of one projection, output into a wider tensor."""
+    import torch
+    rng = np.random.default_rng(13)
+    H, KH, dn, dr, dv, ql, kl = 4, 2, 64, 16, 72, [100, 33], [100, 160]
+    x = prefill_case(rng, H, KH, dn, dr, dv, ql, kl, slack=0)
+    tq, tk = sum(ql), sum(kl)
+    qq = torch.zeros(tq, H, 96, dtype=torch.bfloat16, device=dev)
+    qq[..., :dn], qq[..., 72:72 + dr] = up(x["q"], dev), up(x["qr"], dev)
+    kv = torch.zeros(tk, KH, dn + dv, dtype=torch.bfloat16, device=dev)
+    kv[..., :dn], kv[..., dn:] = up(x["k"], dev).transpose(0, 1), up(x["v"], dev).transpose(0, 1)
+    row = torch.zeros(tk, 40, dtype=torch.bfloat16, device=dev)
+    row[:, 24:] = up(x["kr"], dev)
+    wide = torch.full((tq, H + 1, 80), 3.0, dtype=torch.bfloat16, device=dev)
+    kv_t = kv.transpose(0, 1)
+    got = K.prefill_tensors(qq[..., :dn], qq[..., 72:72 + dr], kv_t[..., :dn], row[:, 24:], kv_t[..., dn:],
+                            i32(starts(ql), dev), i32(starts(kl), dev), 0.1, out=wide[:, :H, :dv])
+    check_prefill(got, x, ql, kl, 0.1, True)
+    assert bool((wide[:, H] == 3.0).all()) and bool((wide[..., dv:] == 3.0).all())
+
+
+def test_prefill_leaves_rows_past_the_last_sequence(dev):
+    import torch
+    rng = np.random.default_rng(14)
+    ql, kl = [130, 5], [130, 9]
+    x = prefill_case(rng, 2, 2, 64, 0, 64, ql, kl, slack=300)
+    out = torch.full((435, 2, 64), 9.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((435, 2), 9.0, dtype=torch.float32, device=dev)
+    got = call(dev, x, ql, kl, 0.1, True, out=out, lse=lse)
+    check_prefill(got, x, ql, kl, 0.1, True)
+    assert bool((out[135:] == 9.0).all()) and bool((lse[135:] == 9.0).all())
+
+
+def test_prefill_nothing_passes_between_sequences(dev):
+    """A sequence whose keys and values are NaN or infinite spoils only itself."""
+    rng = np.random.default_rng(15)
+    ql, kl = [60, 70, 80], [60, 70, 200]
+    x = prefill_case(rng, 2, 2, 128, 64, 128, ql, kl)
+    x["k"][:, 60:130], x["v"][:, 60:100], x["v"][:, 100:130] = W.BF16_NAN, W.BF16_NAN, 0x7F80
+    x["q"][60:130] = W.BF16_NAN
+    for causal in (True, False):
+        check_prefill(call(dev, x, ql, kl, 0.1, causal), x, ql, kl, 0.1, causal, skip=(1,))
+
+
+def test_prefill_bad_starts_set_the_bit(dev):
+    rng = np.random.default_rng(16)
+    x = prefill_case(rng, 1, 1, 64, 0, 64, [50, 60, 70], [50, 60, 70])
+    t = {k: None if v is None else up(v, dev) for k, v in x.items()}
+    for q, k in (([0, 50, 110, 400], [0, 50, 110, 180]), ([0, 50, 110, 180], [0, 50, 110, 400]),
+                 ([0, 50, 110, 90], [0, 50, 110, 180]), ([0, 50, 110, 180], [0, 50, 110, 90])):
+        err = word(dev)
+        got = K.prefill_tensors(t["q"], None, t["k"], None, t["v"], i32(q, dev), i32(k, dev), 0.1, device_error=err)
+        assert int(err.item()) == K.KVATTN_DEVERR_BAD_LENGTH
+        check_prefill(got, x, [50, 60], [50, 60], 0.1, True)
+
+
+def test_prefill_many_sequences(dev):
+    """More sequences than a block of the plan has threads, most of them short."""
+    rng = np.random.default_rng(17)
+    ql = rng.integers(0, 4, 1500).tolist()
+    kl = [a + int(b) for a, b in zip(ql, rng.integers(0, 3, 1500))]
+    x = prefill_case(rng, 1, 1, 64, 0, 64, ql, kl)
+    check_prefill(call(dev, x, ql, kl, 0.1, True), x, ql, kl, 0.1, True)
+
+
+def test_prefill_more_items_than_sms(dev):
+    """Several items a CTA: query tiles, rings and TMEM are taken over from item to item."""
+    rng = np.random.default_rng(18)
+    ql, kl = [700, 3, 390], [700, 260, 520]
+    x = prefill_case(rng, 41, 41, 64, 0, 64, ql, kl)
+    check_prefill(call(dev, x, ql, kl, 0.125, True), x, ql, kl, 0.125, True)
+
+
+def test_prefill_twice_is_the_same_and_streams_do_not_meet(dev):
+    """Two calls at once on two streams, each with its own workspace, and a captured call replayed."""
+    import torch
+    rng = np.random.default_rng(19)
+    ql, kl = [400, 100], [600, 100]
+    x = prefill_case(rng, 8, 8, 128, 64, 128, ql, kl)
+    t = {k: up(v, dev) for k, v in x.items()}
+    qs, ks = i32(starts(ql), dev), i32(starts(kl), dev)
+    torch.cuda.synchronize()
+
+    def go():
+        return K.prefill_tensors(t["q"], t["qr"], t["k"], t["kr"], t["v"], qs, ks, 0.07)["out"][:sum(ql)]
+    one, side = go(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(4):
+        for s in side:
+            with torch.cuda.stream(s):
+                got.append(go())
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        kept = go()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for y in got + [kept]:
+        assert torch.equal(one, y)
+
+
+# ------------------------------------------------------------- all together
+
+@pytest.mark.parametrize("name", ["mla", "gla"])
+def test_a_prompt_then_tokens(dev, name):
+    """Tables, append, expand and prefill of two chunks, then the last token of
+    every sequence through the absorbed decode on the same cache: the expanded
+    and the absorbed form of the same attention.  Both round keys or queries,
+    weights, outputs to bf16 (each <= 2^-8 relative), four roundings apart:
+    relative 2-norm within 1.5e-2, and both within 1e-2 of the fp64 chain."""
+    import torch
+    rng = np.random.default_rng(20)
+    s = W.WORKLOADS[name]
+    H, G, dc, dr, dh = 16, s.num_kv, s.d_nope, s.d_rope, 128
+    B, mpps, pages = 3, 12, 40
+    chunks = [[300, 1, 129], [64, 200, 0]]
+    row = G * dc + dr
+    variant = K.VARIANTS[name]
+    cache = torch.full((pages, 64, row), float("nan"), dtype=torch.bfloat16, device=dev)
+    uk, uv = bits(rng, H, dh, dc, scale=dc ** -0.5), bits(rng, H, dc, dh, scale=dh ** -0.5)
+    tuk, tuv = up(uk, dev), up(uv, dev)
+    lens, table, count = i32([0] * B, dev), i32(np.full((B, mpps), -1), dev), i32([pages], dev)
+    pool = i32(rng.permutation(pages), dev)
+    scale = (dh + dr) ** -0.5
+    past = [np.zeros((0, row))] * B
+    err = word(dev)
+    for new in chunks:
+        T = sum(new)
+        rows, q, qr = bits(rng, T, row), bits(rng, T, H, dh), bits(rng, T, H, dr)
+        tq, tqr = up(q, dev), up(qr, dev)
+        st = K.build_tables_tensors(lens, i32(new, dev), pool, count, table, T + 10, err, inplace=True)
+        p = K.make_params(B, H, G, dc, dr, mpps, pages, 0)
+        K.append_slots_tensor(variant, p, up(rows, dev), st["pos"][:T].contiguous(), st["slots"][:T].contiguous(), cache,
+                              W.ROPE_BASE, err)
+        K.rope_tensor(tqr, st["pos"], 0, dr, W.ROPE_BASE, H)
+        total = int(st["kv_start"][-1])
+        e = K.expand_kv_tensors(variant, p, cache, table, st["kv_start"], tuk, tuv, total, err)
+        got = K.prefill_tensors(tq, tqr, e["k"], e["k_rope"], e["v"], st["q_start"], st["kv_start"], scale, device_error=err)
+        # the fp64 chain
+        at, off, num, den = 0, 0.0, 0.0, 0.0
+        from oracle import steps
+        for b, n in enumerate(new):
+            pos = len(past[b]) + np.arange(n)
+            r = f64(rows[at:at + n])
+            if n:
+                r[:, G * dc:] = steps.rope(r[:, G * dc:], pos, W.ROPE_BASE)
+            past[b] = np.concatenate([past[b], r])
+            k, v, _, _ = prompt.expand(past[b], f64(uk), f64(uv), G)
+            for h in range(H if n else 0):
+                qq = np.concatenate([f64(q[at:at + n, h]), steps.rope(f64(qr[at:at + n, h]), pos, W.ROPE_BASE)], 1)
+                ref = prompt.attention(qq, np.concatenate([k[h], past[b][:, G * dc:]], 1), v[h], scale, True)[0]
+                num += ((down(got["out"][at:at + n, h]) - ref) ** 2).sum()
+                den += (ref ** 2).sum()
+            at += n
+        assert np.sqrt(num / den) <= 1e-2
+    assert int(err.item()) == 0
+    # the newest token of each sequence again, absorbed
+    last = [0, chunks[1][0] + chunks[1][1] - 1]
+    idx = torch.tensor([chunks[1][0] - 1, chunks[1][0] + chunks[1][1] - 1], device=dev)
+    p = K.make_params(2, H, G, dc, dr, mpps, pages, 500)
+    qa = K.head_proj_tensor(tq[idx].contiguous(), tuk)
+    ol = torch.empty(2, H, dc, dtype=torch.bfloat16, device=dev)
+    lse = torch.empty(2, H, dtype=torch.float32, device=dev)
+    ws = torch.zeros(K.kvattn_workspace_size(variant, p), dtype=torch.uint8, device=dev)
+    K.decode_tensors(variant, p, qa, tqr[idx].contiguous(), cache, table, lens, scale, ol, lse, ws)
+    one = down(K.head_proj_tensor(ol, tuv))
+    two = down(got["out"][idx])
+    assert len(last) == 2 and np.linalg.norm(one - two) <= 1.5e-2 * np.linalg.norm(two)
+    # lse of the two forms: keys rounded to bf16 in one, the absorbed query in the other
+    assert np.abs(down(lse) - down(got["lse"][idx])).max() <= 2e-2
