@@ -19,11 +19,12 @@
 // tokens x 64 columns, 128-byte swizzle) that key and value tiles pass through
 // in the order of their use.
 //
-// Warp roles (320 threads):
-//   warp 0     one thread streams queries, keys and values with TMA
+// Warp roles (384 threads):
+//   warp 0     one thread hands out the items and streams queries, keys and
+//              values with TMA
 //   warp 1     one thread issues the MMAs, in the order
 //              S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
-//   warps 2-9  one thread per query row: scores from TMEM, mask, online softmax
+//   warps 4-11 one thread per query row: scores from TMEM, mask, online softmax
 //              in fp32 (base 2), probabilities back to TMEM in bf16, output
 //              rescaled when the maximum grows by more than 2^8 (lazily: the
 //              reference maximum only scales numerator and denominator alike)
@@ -31,10 +32,10 @@
 // the sum uses the unrounded values; scores, maxima, sums and outputs stay in
 // fp32.
 //
-// The work list (tiles by falling number of keys) comes from ragged.cu; CTA c
-// of a grid of one CTA per SM takes items c, c + grid, ... of a list ordered
-// by groups of eight heads, then tiles, then heads, so that the CTAs at work
-// share a few heads' keys and values in L2.
+// The work list (tiles by falling number of keys) comes from ragged.cu; the
+// CTAs, one per SM, take its items as they get to them, ordered by groups of
+// eight heads, then tiles, then heads, so that the CTAs at work share a few
+// heads' keys and values in L2.
 #include <math.h>
 
 #include "latent_common.cuh"
@@ -55,7 +56,12 @@ bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int kTile = 128;                        // query rows of an MMA tile, keys of a key tile
 constexpr int kItemRows = 2 * kTile;              // query rows of a work item
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers: 384 threads are launched with 168 each (the most that fit), the
+// two softmax warpgroups, which hold a row of 128 scores a thread, take theirs
+// from the one that only issues.  88 + 2 * 208 = 3 * 168.
+constexpr int kLaunchRegs = 168, kIssueRegs = 88, kSoftmaxRegs = 208;
+static_assert(kIssueRegs + 2 * kSoftmaxRegs <= 3 * kLaunchRegs, "register split");
 constexpr int kBoxBytes = kTile * 128;            // 128 rows x 64 bf16
 constexpr uint32_t kBoxUnits = kBoxBytes >> 4;
 constexpr int kHeadGroup = 8;
@@ -63,7 +69,7 @@ constexpr int kBarBytes = 1024;
 constexpr int kSmemMax = 227 * 1024;
 
 struct PrefillArgs {
-    const int32_t *header;
+    int32_t *header;                              // [0] tiles, [1] items handed out (0 at the start)
     const ragged::Tile *tiles;
     void *out;
     float *lse;                                   // may be null
@@ -87,14 +93,66 @@ struct Layout {
     static_assert(kRing >= 2 * NKB + NVB, "two key tiles and a value tile in flight");
 };
 
+// The item numbers that the TMA thread hands out, two at a time.
+constexpr int kItemReaders = 9;                   // the MMA warp and the softmax warps
+
 struct Bars {
     uint64_t full[16], empty[16];
+    uint64_t item_full[2], item_empty[2];
+    int32_t item[2];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t mma_done;
     uint32_t tmem_base;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier space");
+
+template <int N>
+__device__ __forceinline__ void set_regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 columns of this thread's TMEM lane; the store is waited for with tmem_st_wait.
+__device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// 32 columns; the values may be used after tmem_ld_wait, which names them.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait(float *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        asm volatile("" : "+f"(r[i]));
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Work item i: its tile, its head, and the key tiles of its two query tiles.
 struct Item {
@@ -155,6 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B.p_full[i], kTile);
             mbar_init(&B.o_full[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.item_full[i], 1);
+            mbar_init(&B.item_empty[i], kItemReaders);
+        }
         mbar_init(&B.mma_done, 1);
         fence_mbar_init();
     }
@@ -169,7 +231,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ntiles = a.header[0];
     const int items = ntiles * a.heads;
     bool ok = true;
+    // The next item, for a whole warp: -1 at the end or where a wait ran out.
+    uint32_t taken = 0;
+    auto next_item = [&]() -> int {
+        const int slot = taken & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&B.item_full[slot], (taken >> 1) & 1))) {
+            ok = false;
+            return -1;
+        }
+        const int i = B.item[slot];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&B.item_empty[slot]);
+        ++taken;
+        return i;
+    };
 
+    if (warp < 4) {
+    set_regs_down<kIssueRegs>();
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA
         if (lane == 0) {
@@ -229,8 +308,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(ring + s * kBoxBytes, &m.v, 64 * (wraps ? 1 - b : b), kvh, row, &B.full[s]);
                 }
             };
-            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            // items are handed out as CTAs get to them: the first by the block's
+            // number, then by a count that the plan kernel sets to 0
+            int i = blockIdx.x;
+            for (uint32_t given = 0;; ++given) {
+                const int slot = given & 1;
+                if (!ok || (given >= 2 && !mbar_wait(&B.item_empty[slot], ((given >> 1) - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                B.item[slot] = i < items ? i : -1;
+                mbar_arrive(&B.item_full[slot]);
+                if (i >= items)
+                    break;
                 const Item it = get_item(a, ntiles, i);
+                i = (int)gridDim.x + atomicAdd(&a.header[1], 1);
                 const int n = max(it.n0, it.n1);
                 if (n == 0)
                     continue;
@@ -266,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);       // K-major query boxes
         const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);       // K-major key boxes
         uint32_t base = 0;                               // ring position of the item's first key tile
-        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};         // query tiles and probability tiles taken
+        uint32_t qpar = 0, ppar = 0;                     // phase bit i: query and probability tiles of query tile i
         auto wait_box = [&](uint32_t pos) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(&B.full[pos % R], (pos / R) & 1));
         };
@@ -274,11 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_s = [&](const Item &it, int i, int j, bool first, bool free) {
             const uint32_t p0 = base + (uint32_t)j * Lay::kStep;
             if (j == 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&B.q_full[i], qn[i] & 1))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&B.q_full[i], (qpar >> i) & 1))) {
                     ok = false;
                     return;
                 }
-                ++qn[i];
+                qpar ^= 1u << i;
             }
 #pragma unroll
             for (int b = 0; b < NKB; ++b) {
@@ -328,11 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(&B.p_full[i], pn[i] & 1))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&B.p_full[i], (ppar >> i) & 1))) {
                 ok = false;
                 return;
             }
-            ++pn[i];
+            ppar ^= 1u << i;
             tc_fence_after();
             if (lane == 0) {
                 const uint32_t s0 = p0 % R, s1 = (p0 + NVB - 1) % R;
@@ -353,23 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = get_item(a, ntiles, i);
+        for (int w; ok && (w = next_item()) >= 0;) {
+            const Item it = get_item(a, ntiles, w);
             const int n = max(it.n0, it.n1);
-            if (it.n0 > 0)
-                issue_s(it, 0, 0, true, it.n1 == 0);
-            if (ok && it.n1 > 0)
-                issue_s(it, 1, 0, it.n0 == 0, true);
-            for (int j = 0; ok && j < n; ++j) {
-                const bool in0 = j < it.n0, in1 = j < it.n1, next0 = j + 1 < it.n0, next1 = j + 1 < it.n1;
-                if (in0)
-                    issue_pv(it, 0, j, true, !in1);
-                if (ok && next0)
-                    issue_s(it, 0, j + 1, true, !next1);
-                if (ok && in1)
-                    issue_pv(it, 1, j, !in0, true);
-                if (ok && next1)
-                    issue_s(it, 1, j + 1, !next0, true);
+            // per key tile and query tile: P.V of this tile, scores of the next
+#pragma unroll 1
+            for (int x = -2; ok && x < 2 * n; ++x) {
+                const int j = x >> 1, i = x & 1;
+                const int mine = i ? it.n1 : it.n0, other = i ? it.n0 : it.n1;
+                // the first query tile with keys in a tile waits for its boxes, the last one frees them
+                if (j >= 0 && j < mine)
+                    issue_pv(it, i, j, i == 0 || j >= other, i == 1 || j >= other);
+                if (ok && j + 1 < mine)
+                    issue_s(it, i, j + 1, i == 0 || j + 1 >= other, i == 1 || j + 1 >= other);
             }
             base += (uint32_t)n * Lay::kStep;
         }
@@ -382,20 +470,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&B.mma_done, 0) && lane == 0 && a.err)
             atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
         __syncwarp();
+    }
     } else {
+        set_regs_up<kSoftmaxRegs>();
         // ------------------------------------------------------------ softmax
-        const int i = (warp - 2) >> 2;                   // query tile
+        const int i = (warp >> 2) - 1;                   // query tile
         const int quarter = warp & 3;
         const int row = i * kTile + quarter * 32 + lane; // of the item
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tS + i * kTile + lane_addr, o_addr = tO + i * kTile + lane_addr;
-        const bool flat = a.scale_log2 == 0.f;           // every key weighs the same
-        const float c = flat ? 1.f : a.scale_log2;
+        const float c = a.scale_log2;
         uint32_t sn = 0, on = 0;                         // score tiles and outputs taken
-        for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-            const Item it = get_item(a, ntiles, w);
-            const int n = i ? it.n1 : it.n0;
-            const int lim = a.causal ? min(it.t.nk, it.t.lim0 + row) : it.t.nk;
+        for (int w; ok && (w = next_item()) >= 0;) {
+            int n, lim;
+            {
+                const Item it = get_item(a, ntiles, w);
+                n = i ? it.n1 : it.n0;
+                lim = a.causal ? min(it.t.nk, it.t.lim0 + row) : it.t.nk;
+            }
             const int lim_first = __shfl_sync(0xffffffffu, lim, 0);     // limits grow with the row
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
@@ -405,18 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++sn;
                 tc_fence_after();
                 float s[kTile];
-                {
-                    uint32_t r[kTile];
-                    tmem_ld128(s_addr, r);
 #pragma unroll
-                    for (int x = 0; x < kTile; ++x)
-                        s[x] = __uint_as_float(r[x]);
-                }
-                if (flat) {
+                for (int x = 0; x < kTile; x += 32)
+                    tmem_ld32_start(s_addr + x, s + x);
 #pragma unroll
-                    for (int x = 0; x < kTile; ++x)
-                        s[x] *= 0.f;
-                }
+                for (int x = 0; x < kTile; x += 32)
+                    tmem_ld_wait(s + x);
                 // raw scores: the scale is folded into the exponent's FMA; for
                 // a negative scale the row's maximum is at the lowest score
                 const int nvalid = lim - j * kTile;
@@ -445,18 +531,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                 float sx[4] = {0.f, 0.f, 0.f, 0.f}, sy[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t pk[kTile / 2];
 #pragma unroll
-                for (int x = 0; x < kTile / 2; ++x) {
-                    float x0, x1;
-                    ffma2(x0, x1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
-                    const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
-                    fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
-                    const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
-                    pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
+                for (int y = 0; y < kTile; y += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        float x0, x1;
+                        ffma2(x0, x1, s[y + 2 * x], s[y + 2 * x + 1], c, c, nm, nm);
+                        const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
+                        fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
+                        const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
+                        pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
+                    }
+                    tmem_st16_start(s_addr + y / 2, pk);
                 }
                 l = l * alpha + (((sx[0] + sy[0]) + (sx[1] + sy[1])) + ((sx[2] + sy[2]) + (sx[3] + sy[3])));
-                tmem_st64(s_addr, pk);
+                tmem_st_wait();
                 // the scores' commit covers every earlier P.V, so the output
                 // holds all tiles before this one; TMEM accesses are
                 // warp-wide: the warp's rows are rescaled when any needs it
@@ -483,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++on;
                 tc_fence_after();
             }
+            const Item it = get_item(a, ntiles, w);      // again: kept, it would cost the loop its registers
             const bool valid = row < it.t.nq;
             const bool any = n > 0 && l != 0.f;          // a row without keys has l = 0 (NaN passes)
             const float inv = any ? 1.f / l : 0.f;
@@ -551,6 +642,13 @@ cudaError_t launch(const Call &c)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
+    // the register split waits for good if the kernel is launched with fewer
+    static const int regs = [](const void *f) {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, f) == cudaSuccess ? at.numRegs : 0;
+    }(reinterpret_cast<const void *>(kern));
+    if (regs != kLaunchRegs)
+        return cudaErrorInvalidConfiguration;
     const long long sms = sm_count();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c.most_items < sms ? c.most_items : sms));
@@ -698,7 +796,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     a.causal = p->causal;
     a.out_token_stride = so[0];
     a.out_head_stride = so[1];
-    a.scale_log2 = sm_scale * 1.4426950408889634f;
+    // masked scores are infinite, so a scale of 0 (every key weighs the same)
+    // is taken as one too small to show in any weight
+    a.scale_log2 = sm_scale == 0.f ? 1e-30f : sm_scale * 1.4426950408889634f;
     c.most_items = pa.capacity * H;
 
     const int nkn = (p->d_nope + 63) / 64, nvb = (p->d_v + 63) / 64;

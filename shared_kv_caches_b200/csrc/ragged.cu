@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanArgs a)
     if (tid == 0) {
         start[a.batch] = n;
         a.header[0] = n;
+        a.header[1] = 0;
     }
     __syncthreads();
 

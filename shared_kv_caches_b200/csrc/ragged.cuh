@@ -65,7 +65,7 @@ struct Tile {
     int32_t pad;
 };
 
-constexpr size_t kPlanHeader = 256;      // bytes in front of the tile list; its first int counts the tiles
+constexpr size_t kPlanHeader = 256;      // bytes in front of the tile list: [0] its length, [1] 0 (a count for its reader)
 
 struct PlanArgs {
     int batch, rows_per_tile;
