@@ -130,6 +130,34 @@ __device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t *
         : "memory");
 }
 
+// MMAs and commits issued by one elected lane (always the same one) in code
+// that the whole warp runs.  What the descriptors are made of is then the same
+// in every lane and stays in uniform registers: issued from a branch that only
+// lane 0 takes, every operand is moved there first, and an MMA of 64 cycles
+// took 140 to issue (clock trace of an 8K prompt); so, about 70.
+__device__ __forceinline__ void elect_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void elect_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void elect_commit(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 // 32 columns; the values may be used after tmem_ld_wait, which names them.
 __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float *r)
 {
@@ -195,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *const ring = smem + 2 * NKB * kBoxBytes;
     Bars &B = *reinterpret_cast<Bars *>(ring + R * kBoxBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && a.err)
             atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
@@ -358,12 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);       // K-major query boxes
         const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);       // K-major key boxes
         uint32_t base = 0;                               // ring position of the item's first key tile
+        int n0 = 0, n1 = 0, nk = 0;                      // the item's key tiles and keys
         uint32_t qpar = 0, ppar = 0;                     // phase bit i: query and probability tiles of query tile i
         auto wait_box = [&](uint32_t pos) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(&B.full[pos % R], (pos / R) & 1));
         };
         // scores of query tile i and key tile j; free: the last use of the keys
-        auto issue_s = [&](const Item &it, int i, int j, bool first, bool free) {
+        auto issue_s = [&](int i, int j, bool first, bool free) {
             const uint32_t p0 = base + (uint32_t)j * Lay::kStep;
             if (j == 0) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&B.q_full[i], (qpar >> i) & 1))) {
@@ -379,26 +408,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t s = (p0 + b) % R;
-                    const uint64_t qd = qdesc + (uint64_t)((i * NKB + b) * kBoxUnits);
-                    const uint64_t kd = kdesc + (uint64_t)(s * kBoxUnits);
+                const uint32_t s = (p0 + b) % R;
+                const uint64_t qd = qdesc + (uint64_t)((i * NKB + b) * kBoxUnits);
+                const uint64_t kd = kdesc + (uint64_t)(s * kBoxUnits);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_ss(tS + i * kTile, qd + k * 2, kd + k * 2, kIdescS, (b | k) ? 1u : 0u);
-                    if (free)
-                        umma_commit(&B.empty[s]);
-                }
-                __syncwarp();
+                for (int k = 0; k < 4; ++k)
+                    elect_ss(tS + i * kTile, qd + k * 2, kd + k * 2, kIdescS, (b | k) ? 1u : 0u);
+                if (free)
+                    elect_commit(&B.empty[s]);
             }
-            if (lane == 0) {
-                umma_commit(&B.s_full[i]);
-                if (j + 1 == (i ? it.n1 : it.n0))
-                    umma_commit(&B.q_empty[i]);
-            }
-            __syncwarp();
+            elect_commit(&B.s_full[i]);
+            if (j + 1 == (i ? n1 : n0))
+                elect_commit(&B.q_empty[i]);
         };
-        auto issue_pv = [&](const Item &it, int i, int j, bool first, bool free) {
+        auto issue_pv = [&](int i, int j, bool first, bool free) {
             const uint32_t p0 = base + (uint32_t)j * Lay::kStep + NKB;
             if (first) {
 #pragma unroll
@@ -409,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 // value rows past the sequence are zeroed: their probabilities
                 // are 0, and 0 * NaN would poison the output
-                const int ntok = it.t.nk - j * kTile;
+                const int ntok = nk - j * kTile;
                 if (ntok < kTile) {
                     for (int idx = lane; idx < (kTile - ntok) * 8 * NVB; idx += 32) {
                         const int b = idx / ((kTile - ntok) * 8), rem = idx % ((kTile - ntok) * 8);
@@ -426,47 +449,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ppar ^= 1u << i;
             tc_fence_after();
-            if (lane == 0) {
+            {
                 const uint32_t s0 = p0 % R, s1 = (p0 + NVB - 1) % R;
                 const uint32_t lo = s0 < s1 ? s0 : s1, hi = s0 < s1 ? s1 : s0;
                 const uint64_t vd = smem_desc(smem_u32(ring) + lo * kBoxBytes,
                                               NVB == 2 ? (hi - lo) * kBoxBytes : kBoxBytes, 1024, 2);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
-                    umma_ts(tO + i * kTile, tS + i * kTile + 8 * k, vd + (uint64_t)(k * 128), kIdescPV,
+                    elect_ts(tO + i * kTile, tS + i * kTile + 8 * k, vd + (uint64_t)(k * 128), kIdescPV,
                             (j > 0 || k > 0) ? 1u : 0u);
                 if (free) {
-                    umma_commit(&B.empty[s0]);
+                    elect_commit(&B.empty[s0]);
                     if (NVB == 2)
-                        umma_commit(&B.empty[s1]);
+                        elect_commit(&B.empty[s1]);
                 }
-                if (j + 1 == (i ? it.n1 : it.n0))
-                    umma_commit(&B.o_full[i]);
+                if (j + 1 == (i ? n1 : n0))
+                    elect_commit(&B.o_full[i]);
             }
-            __syncwarp();
         };
         for (int w; ok && (w = next_item()) >= 0;) {
-            const Item it = get_item(a, ntiles, w);
-            const int n = max(it.n0, it.n1);
+            {
+                const Item it = get_item(a, ntiles, w);
+                n0 = __shfl_sync(0xffffffffu, it.n0, 0);
+                n1 = __shfl_sync(0xffffffffu, it.n1, 0);
+                nk = __shfl_sync(0xffffffffu, it.t.nk, 0);
+            }
+            const int n = max(n0, n1);
             // per key tile and query tile: P.V of this tile, scores of the next
 #pragma unroll 1
             for (int x = -2; ok && x < 2 * n; ++x) {
                 const int j = x >> 1, i = x & 1;
-                const int mine = i ? it.n1 : it.n0, other = i ? it.n0 : it.n1;
+                const int mine = i ? n1 : n0, other = i ? n0 : n1;
                 // the first query tile with keys in a tile waits for its boxes, the last one frees them
                 if (j >= 0 && j < mine)
-                    issue_pv(it, i, j, i == 0 || j >= other, i == 1 || j >= other);
+                    issue_pv(i, j, i == 0 || j >= other, i == 1 || j >= other);
                 if (ok && j + 1 < mine)
-                    issue_s(it, i, j + 1, i == 0 || j + 1 >= other, i == 1 || j + 1 >= other);
+                    issue_s(i, j + 1, i == 0 || j + 1 >= other, i == 1 || j + 1 >= other);
             }
             base += (uint32_t)n * Lay::kStep;
         }
         if (!ok && lane == 0 && a.err)
             atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
         // every MMA this thread issued has completed before TMEM is freed
-        if (lane == 0)
-            umma_commit(&B.mma_done);
-        __syncwarp();
+        elect_commit(&B.mma_done);
         if (!mbar_wait(&B.mma_done, 0) && lane == 0 && a.err)
             atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
         __syncwarp();
