@@ -6,24 +6,29 @@
 //   o_i  = sum_j softmax_j(s_ij) v_j        over j < nk (causal: j <= i + nk - nq)
 //
 // One CTA works off 256 query rows of one head (two MMA tiles of 128) against
-// key tiles of 128 tokens in one pass with a running maximum and sum.  Per key
-// tile and query tile the tensor cores need 64 cycles for each 16 columns of
-// the key width and each 16 tokens of P.V (1280 cycles for 192 / 128) and the
-// special-function units 1024 cycles for 128 x 128 exponentials (16 per cycle
-// and SM), so the two query tiles take turns: while one's softmax runs, the
-// other's MMAs do.
+// key tiles of 96 tokens in one pass with a running maximum and sum.  Per key
+// tile and query tile the tensor cores need 960 cycles for a key of 192 and a
+// value of 128 (12 MMAs of N = 96, 6 of N = 128), the special-function units
+// 768 for 128 x 96 exponentials at 16 a cycle, of which a quarter is moved to
+// the FMA pipe.  A softmax step takes longer than the MMAs of a tile from
+// start to end, so everything that can is taken off the path between two
+// steps of a query tile: its next scores are formed while its softmax runs
+// (the scores' columns are free as soon as they are in registers), and the
+// other query tile's MMAs fill what is left.
 //
-// TMEM (512 columns): scores of the two tiles (128 each; the bf16
-// probabilities overwrite the first half), outputs of the two tiles (128
-// each).  Shared memory: the two query tiles, and a ring of 16 KB boxes (128
-// tokens x 64 columns, 128-byte swizzle) that key and value tiles pass through
-// in the order of their use.
+// TMEM (512 columns): outputs of the two query tiles (128 each), their scores
+// (96 each), and one tile of bf16 probabilities (48) that the two take turns
+// with; keys come in tiles of 96, not 128, so that all of it fits.  Shared
+// memory: the two query tiles, two key tiles and two value tiles, in boxes of 64
+// columns (128-byte swizzle).
 //
 // Warp roles (384 threads):
 //   warp 0     one thread hands out the items and streams queries, keys and
 //              values with TMA
-//   warp 1     one thread issues the MMAs, in the order
-//              S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
+//   warp 1     issues the MMAs of the scores, S0(j) S1(j) S0(j+1) ...
+//   warp 2     issues those of P.V, PV0(j) PV1(j) PV0(j+1) ... (a warp of its
+//              own: one that issued both spent more time on the waits and
+//              commits between them than the MMAs take)
 //   warps 4-11 one thread per query row: scores from TMEM, mask, online softmax
 //              in fp32 (base 2), probabilities back to TMEM in bf16, output
 //              rescaled when the maximum grows by more than 2^8 (lazily: the
@@ -54,16 +59,18 @@ using latent::reduce_extreme;
 
 bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-constexpr int kTile = 128;                        // query rows of an MMA tile, keys of a key tile
+constexpr int kTile = 128;                        // query rows of an MMA tile
+constexpr int kKeys = 96;                         // keys of a key tile
 constexpr int kItemRows = 2 * kTile;              // query rows of a work item
 constexpr int kThreads = 384;
 // Registers: 384 threads are launched with 168 each (the most that fit), the
-// two softmax warpgroups, which hold a row of 128 scores a thread, take theirs
+// two softmax warpgroups, which hold a row of scores a thread, take theirs
 // from the one that only issues.  88 + 2 * 208 = 3 * 168.
 constexpr int kLaunchRegs = 168, kIssueRegs = 88, kSoftmaxRegs = 208;
 static_assert(kIssueRegs + 2 * kSoftmaxRegs <= 3 * kLaunchRegs, "register split");
-constexpr int kBoxBytes = kTile * 128;            // 128 rows x 64 bf16
-constexpr uint32_t kBoxUnits = kBoxBytes >> 4;
+constexpr int kQBox = kTile * 128;                // 128 query rows x 64 bf16
+constexpr int kBox = kKeys * 128;                 // 96 keys x 64 bf16
+constexpr int kExpCycle = 4, kExpFma = 1;         // of four pairs of exponentials, one on the FMA pipe
 constexpr int kHeadGroup = 8;
 constexpr int kBarBytes = 1024;
 constexpr int kSmemMax = 227 * 1024;
@@ -87,22 +94,27 @@ struct Maps {
 // NKB key boxes (the last one the rope part if ROPE), NVB value boxes.
 template <int NKB, int NVB>
 struct Layout {
-    static constexpr int kRing = (kSmemMax - kBarBytes - 2 * NKB * kBoxBytes) / kBoxBytes;
-    static constexpr int kStep = NKB + NVB;       // boxes of a key tile and its value tile
-    static constexpr size_t kBytes = (size_t)(2 * NKB + kRing) * kBoxBytes + kBarBytes;
-    static_assert(kRing >= 2 * NKB + NVB, "two key tiles and a value tile in flight");
+    static constexpr int kKeyTile = NKB * kBox, kValueTile = NVB * kBox;
+    static constexpr size_t kKeysAt = (size_t)2 * NKB * kQBox;
+    static constexpr size_t kValuesAt = kKeysAt + 2 * kKeyTile;
+    static constexpr size_t kBarsAt = kValuesAt + 2 * kValueTile;
+    static constexpr size_t kBytes = kBarsAt + kBarBytes;
+    static_assert(kBytes <= kSmemMax, "shared memory");
 };
 
 // The item numbers that the TMA thread hands out, two at a time.
-constexpr int kItemReaders = 9;                   // the MMA warp and the softmax warps
+constexpr int kItemReaders = 10;                  // the MMA warps and the softmax warps
 
 struct Bars {
-    uint64_t full[16], empty[16];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t item_full[2], item_empty[2];
     int32_t item[2];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t mma_done;
+    uint64_t s_full[2], s_free[2];                // scores formed; scores in registers
+    uint64_t p_full[2];                           // probabilities stored
+    uint64_t p_free[2];                           // every P.V before this query tile's next one is done
+    uint64_t o_full[2];                           // the item's last P.V of the query tile is done
+    uint64_t mma_done[2];
     uint32_t tmem_base;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier space");
@@ -182,6 +194,38 @@ __device__ __forceinline__ void tmem_ld_wait(float *r)
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// d = a * b on two fp32 lanes at once
+__device__ __forceinline__ void fmul2(float &dx, float &dy, float ax, float ay, float bx, float by)
+{
+    asm("{\n\t.reg .b64 a2, b2, d2;\n\tmov.b64 a2, {%2, %3};\n\tmov.b64 b2, {%4, %5};\n\t"
+        "mul.rn.f32x2 d2, a2, b2;\n\tmov.b64 {%0, %1}, d2;\n\t}"
+        : "=f"(dx), "=f"(dy)
+        : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+
+// 2^x of two values on the FMA pipe, for x <= 127: x = n + f with n the nearest
+// whole number (read from the low bits of x + 1.5 * 2^23), 2^f on [-1/2, 1/2]
+// by a quartic, scaled by 2^n.  Its coefficients minimise the relative error
+// for a constant term of 1: 2.9e-6, against the 2^-9 that P is rounded with
+// and within what the sum's fp32 additions lose.  x at or below -127 gives
+// exactly 0 (masked keys); NaN stays NaN.
+__device__ __forceinline__ void exp2_fma(float &e0, float &e1, float x0, float x1)
+{
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));      // -127
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
+    constexpr float kRound = 12582912.f;
+    float t0, t1, f0, f1, p0, p1;
+    fadd2(t0, t1, x0, x1, kRound, kRound);
+    fadd2(f0, f1, t0, t1, -kRound, -kRound);
+    ffma2(f0, f1, f0, f1, -1.f, -1.f, x0, x1);
+    ffma2(p0, p1, f0, f1, 0.009585382416844368f, 0.009585382416844368f, 0.05590662732720375f, 0.05590662732720375f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.24024038016796112f, 0.24024038016796112f);
+    ffma2(p0, p1, p0, p1, f0, f1, 0.6931241750717163f, 0.6931241750717163f);
+    ffma2(p0, p1, p0, p1, f0, f1, 1.f, 1.f);
+    fmul2(e0, e1, p0, p1, __uint_as_float((__float_as_uint(t0) << 23) + 0x3F800000u),
+          __uint_as_float((__float_as_uint(t1) << 23) + 0x3F800000u));
+}
+
 // Work item i: its tile, its head, and the key tiles of its two query tiles.
 struct Item {
     ragged::Tile t;
@@ -205,8 +249,8 @@ __device__ __forceinline__ Item get_item(const PrefillArgs &a, int ntiles, int i
     const int hc = min(kHeadGroup, a.heads - g * kHeadGroup);
     it.t = a.tiles[r / hc];
     it.head = g * kHeadGroup + r % hc;
-    it.n0 = (key_end(a, it.t, 0, min(it.t.nq, kTile)) + kTile - 1) / kTile;
-    it.n1 = (key_end(a, it.t, kTile, it.t.nq - kTile) + kTile - 1) / kTile;
+    it.n0 = (key_end(a, it.t, 0, min(it.t.nq, kTile)) + kKeys - 1) / kKeys;
+    it.n1 = (key_end(a, it.t, kTile, it.t.nq - kTile) + kKeys - 1) / kKeys;
     return it;
 }
 
@@ -215,14 +259,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ Maps m, const PrefillArgs a)
 {
     using Lay = Layout<NKB, NVB>;
-    constexpr int R = Lay::kRing;
     constexpr int NKN = ROPE ? NKB - 1 : NKB;
     constexpr int kDv = NVB * 64;
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile, false, false);
+    constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kKeys, false, false);
     constexpr uint32_t kIdescPV = idesc_bf16_f32(kTile, kDv, false, true);
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *const ring = smem + 2 * NKB * kBoxBytes;
-    Bars &B = *reinterpret_cast<Bars *>(ring + R * kBoxBytes);
+    Bars &B = *reinterpret_cast<Bars *>(smem + Lay::kBarsAt);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && a.err)
@@ -230,22 +272,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < R; ++s) {
-            mbar_init(&B.full[s], 1);
-            mbar_init(&B.empty[s], 1);
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.k_full[i], 1);
+            mbar_init(&B.k_empty[i], 1);
+            mbar_init(&B.v_full[i], 1);
+            mbar_init(&B.v_empty[i], 1);
             mbar_init(&B.q_full[i], 1);
             mbar_init(&B.q_empty[i], 1);
             mbar_init(&B.s_full[i], 1);
-            mbar_init(&B.p_full[i], kTile);
+            mbar_init(&B.s_free[i], 4);
+            mbar_init(&B.p_full[i], 4);
+            mbar_init(&B.p_free[i], 1);
             mbar_init(&B.o_full[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&B.item_full[i], 1);
             mbar_init(&B.item_empty[i], kItemReaders);
         }
-        mbar_init(&B.mma_done, 1);
+        mbar_init(&B.mma_done[0], 1);
+        mbar_init(&B.mma_done[1], 1);
         fence_mbar_init();
     }
     if (warp == 0)
@@ -254,7 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = B.tmem_base;
-    const uint32_t tS = tbase, tO = tbase + 2 * kTile;   // + kTile for the second query tile
+    const uint32_t tO = tbase;                           // + 128 for the second query tile
+    const uint32_t tS = tbase + 256;                     // + kKeys for the second query tile
+    const uint32_t tP = tS + 2 * kKeys;
     pdl_wait_primary();                                  // the tile list
     const int ntiles = a.header[0];
     const int items = ntiles * a.heads;
@@ -275,30 +322,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         return i;
     };
 
+    // Every MMA that this warp issued has completed (before TMEM is freed).
+    auto finish = [&]() {
+        elect_commit(&B.mma_done[warp - 1]);
+        ok = __all_sync(0xffffffffu, mbar_wait(&B.mma_done[warp - 1], 0)) && ok;
+        if (!ok && lane == 0 && a.err)
+            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+    };
+
     if (warp < 4) {
     set_regs_down<kIssueRegs>();
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA
         if (lane == 0) {
-            uint32_t pos = 0;                            // boxes put into the ring
+            uint32_t kn = 0, vn = 0;                     // key and value tiles loaded
             uint32_t qn[2] = {0, 0};                     // query tiles loaded
-            auto slot = [&]() -> int {
-                const int s = (int)(pos % R);
-                if (pos >= R && !mbar_wait(&B.empty[s], ((pos / R) - 1) & 1))
-                    ok = false;
-                return s;
-            };
             auto load_q = [&](const Item &it, int i) {
                 if (qn[i] > 0 && !mbar_wait(&B.q_empty[i], (qn[i] - 1) & 1)) {
                     ok = false;
                     return;
                 }
                 ++qn[i];
-                mbar_arrive_expect_tx(&B.q_full[i], NKB * kBoxBytes);
+                mbar_arrive_expect_tx(&B.q_full[i], NKB * kQBox);
                 const int row = it.t.q0 + i * kTile;
 #pragma unroll
                 for (int b = 0; b < NKB; ++b) {
-                    unsigned char *dst = smem + (i * NKB + b) * kBoxBytes;
+                    unsigned char *dst = smem + (i * NKB + b) * kQBox;
                     if (b < NKN)
                         tma_load_3d(dst, &m.q, 64 * b, it.head, row, &B.q_full[i]);
                     else
@@ -306,35 +355,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto load_k = [&](const Item &it, int j) {
-                const int row = it.t.k0 + j * kTile, kvh = it.head / a.heads_per_kv;
+                const int row = it.t.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = kn & 1;
+                if (kn >= 2 && !mbar_wait(&B.k_empty[st], ((kn >> 1) - 1) & 1)) {
+                    ok = false;
+                    return;
+                }
+                ++kn;
+                unsigned char *dst = smem + Lay::kKeysAt + st * Lay::kKeyTile;
+                mbar_arrive_expect_tx(&B.k_full[st], Lay::kKeyTile);
 #pragma unroll
                 for (int b = 0; b < NKB; ++b) {
-                    const int s = slot();
-                    if (!ok)
-                        return;
-                    ++pos;
-                    mbar_arrive_expect_tx(&B.full[s], kBoxBytes);
                     if (b < NKN)
-                        tma_load_3d(ring + s * kBoxBytes, &m.k, 64 * b, kvh, row, &B.full[s]);
+                        tma_load_3d(dst + b * kBox, &m.k, 64 * b, kvh, row, &B.k_full[st]);
                     else
-                        tma_load_2d(ring + s * kBoxBytes, &m.kr, 0, row, &B.full[s]);
+                        tma_load_2d(dst + b * kBox, &m.kr, 0, row, &B.k_full[st]);
                 }
             };
-            // The P.V descriptor steps from the first 64 columns' box to the
-            // next one's by a positive offset, so where the pair wraps around
-            // the ring the lower slot takes the first columns.
             auto load_v = [&](const Item &it, int j) {
-                const int row = it.t.k0 + j * kTile, kvh = it.head / a.heads_per_kv;
-#pragma unroll
-                for (int b = 0; b < NVB; ++b) {
-                    const int s = slot();
-                    if (!ok)
-                        return;
-                    const bool wraps = NVB == 2 && (int)((pos - b) % R) == R - 1;
-                    ++pos;
-                    mbar_arrive_expect_tx(&B.full[s], kBoxBytes);
-                    tma_load_3d(ring + s * kBoxBytes, &m.v, 64 * (wraps ? 1 - b : b), kvh, row, &B.full[s]);
+                const int row = it.t.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = vn & 1;
+                if (vn >= 2 && !mbar_wait(&B.v_empty[st], ((vn >> 1) - 1) & 1)) {
+                    ok = false;
+                    return;
                 }
+                ++vn;
+                unsigned char *dst = smem + Lay::kValuesAt + st * Lay::kValueTile;
+                mbar_arrive_expect_tx(&B.v_full[st], Lay::kValueTile);
+#pragma unroll
+                for (int b = 0; b < NVB; ++b)
+                    tma_load_3d(dst + b * kBox, &m.v, 64 * b, kvh, row, &B.v_full[st]);
             };
             // items are handed out as CTAs get to them: the first by the block's
             // number, then by a count that the plan kernel sets to 0
@@ -360,114 +408,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load_k(it, 0);
                 if (ok && it.n1 > 0)
                     load_q(it, 1);
-                if (ok)
-                    load_v(it, 0);
-                for (int j = 1; ok && j < n; ++j) {
-                    load_k(it, j);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n)
+                        load_k(it, j + 1);
                     if (ok)
                         load_v(it, j);
                 }
             }
             // every copy started here has landed before the CTA can exit
-            for (int s = 0; s < R && s < (int)min(pos, (uint32_t)R); ++s) {
-                const uint32_t uses = (pos - 1 - s) / R;         // full phases before the slot's last
-                if (!mbar_wait(&B.full[s], uses & 1))
+            for (uint32_t st = 0; st < 2; ++st) {
+                // phase of the stage's last load
+                if (kn > st && !mbar_wait(&B.k_full[st], ((kn - 1 - st) >> 1) & 1))
+                    ok = false;
+                if (vn > st && !mbar_wait(&B.v_full[st], ((vn - 1 - st) >> 1) & 1))
+                    ok = false;
+                if (qn[st] > 0 && !mbar_wait(&B.q_full[st], (qn[st] - 1) & 1))
                     ok = false;
             }
-            for (int i = 0; i < 2; ++i)
-                if (qn[i] > 0 && !mbar_wait(&B.q_full[i], (qn[i] - 1) & 1))
-                    ok = false;
             if (!ok && a.err)
                 atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA
-        const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);       // K-major query boxes
-        const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);       // K-major key boxes
-        uint32_t base = 0;                               // ring position of the item's first key tile
-        int n0 = 0, n1 = 0, nk = 0;                      // the item's key tiles and keys
-        uint32_t qpar = 0, ppar = 0;                     // phase bit i: query and probability tiles of query tile i
-        auto wait_box = [&](uint32_t pos) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait(&B.full[pos % R], (pos / R) & 1));
-        };
-        // scores of query tile i and key tile j; free: the last use of the keys
-        auto issue_s = [&](int i, int j, bool first, bool free) {
-            const uint32_t p0 = base + (uint32_t)j * Lay::kStep;
-            if (j == 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&B.q_full[i], (qpar >> i) & 1))) {
-                    ok = false;
-                    return;
-                }
-                qpar ^= 1u << i;
-            }
-#pragma unroll
-            for (int b = 0; b < NKB; ++b) {
-                if (first && !wait_box(p0 + b)) {
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
-                const uint32_t s = (p0 + b) % R;
-                const uint64_t qd = qdesc + (uint64_t)((i * NKB + b) * kBoxUnits);
-                const uint64_t kd = kdesc + (uint64_t)(s * kBoxUnits);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    elect_ss(tS + i * kTile, qd + k * 2, kd + k * 2, kIdescS, (b | k) ? 1u : 0u);
-                if (free)
-                    elect_commit(&B.empty[s]);
-            }
-            elect_commit(&B.s_full[i]);
-            if (j + 1 == (i ? n1 : n0))
-                elect_commit(&B.q_empty[i]);
-        };
-        auto issue_pv = [&](int i, int j, bool first, bool free) {
-            const uint32_t p0 = base + (uint32_t)j * Lay::kStep + NKB;
-            if (first) {
-#pragma unroll
-                for (int b = 0; b < NVB; ++b)
-                    if (!wait_box(p0 + b)) {
-                        ok = false;
-                        return;
-                    }
-                // value rows past the sequence are zeroed: their probabilities
-                // are 0, and 0 * NaN would poison the output
-                const int ntok = nk - j * kTile;
-                if (ntok < kTile) {
-                    for (int idx = lane; idx < (kTile - ntok) * 8 * NVB; idx += 32) {
-                        const int b = idx / ((kTile - ntok) * 8), rem = idx % ((kTile - ntok) * 8);
-                        *reinterpret_cast<uint4 *>(ring + ((p0 + b) % R) * kBoxBytes + (ntok + rem / 8) * 128 +
-                                                   (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(&B.p_full[i], (ppar >> i) & 1))) {
-                ok = false;
-                return;
-            }
-            ppar ^= 1u << i;
-            tc_fence_after();
-            {
-                const uint32_t s0 = p0 % R, s1 = (p0 + NVB - 1) % R;
-                const uint32_t lo = s0 < s1 ? s0 : s1, hi = s0 < s1 ? s1 : s0;
-                const uint64_t vd = smem_desc(smem_u32(ring) + lo * kBoxBytes,
-                                              NVB == 2 ? (hi - lo) * kBoxBytes : kBoxBytes, 1024, 2);
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    elect_ts(tO + i * kTile, tS + i * kTile + 8 * k, vd + (uint64_t)(k * 128), kIdescPV,
-                            (j > 0 || k > 0) ? 1u : 0u);
-                if (free) {
-                    elect_commit(&B.empty[s0]);
-                    if (NVB == 2)
-                        elect_commit(&B.empty[s1]);
-                }
-                if (j + 1 == (i ? n1 : n0))
-                    elect_commit(&B.o_full[i]);
-            }
-        };
+        // ------------------------------------------------------------- scores
+        const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);                           // K-major query boxes
+        const uint64_t kdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kKeysAt, 16, 1024, 2);  // K-major key boxes
+        uint32_t t = 0;                                  // key tiles of the items before
+        // phase bit i of query tile i: queries, scores taken to registers (the
+        // first tile's columns are free from the start)
+        uint32_t qpar = 0, fpar = 3;
         for (int w; ok && (w = next_item()) >= 0;) {
+            int n0, n1;
+            {
+                const Item it = get_item(a, ntiles, w);
+                n0 = __shfl_sync(0xffffffffu, it.n0, 0);
+                n1 = __shfl_sync(0xffffffffu, it.n1, 0);
+            }
+            const int n = max(n0, n1);
+#pragma unroll 1
+            for (int x = 0; x < 2 * n; ++x) {
+                const int j = x >> 1, i = x & 1;
+                const int mine = i ? n1 : n0, other = i ? n0 : n1;
+                if (j >= mine)
+                    continue;
+                const uint32_t st = (t + j) & 1;
+                bool in = true;
+                if (i == 0 || j >= other)                // the first of the tile's uses
+                    in = mbar_wait(&B.k_full[st], ((t + j) >> 1) & 1);
+                if (j == 0) {
+                    in = in && mbar_wait(&B.q_full[i], (qpar >> i) & 1);
+                    qpar ^= 1u << i;
+                }
+                in = in && mbar_wait(&B.s_free[i], (fpar >> i) & 1);
+                fpar ^= 1u << i;
+                ok = __all_sync(0xffffffffu, in);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t qd = qdesc + (uint64_t)(i * NKB * (kQBox >> 4));
+                const uint64_t kd = kdesc + (uint64_t)(st * (Lay::kKeyTile >> 4));
+#pragma unroll
+                for (int k = 0; k < 4 * NKB; ++k)
+                    elect_ss(tS + i * kKeys, qd + (k / 4) * (kQBox >> 4) + (k % 4) * 2,
+                             kd + (k / 4) * (kBox >> 4) + (k % 4) * 2, kIdescS, k ? 1u : 0u);
+                elect_commit(&B.s_full[i]);
+                if (i == 1 || j >= other)                // the last of the tile's uses
+                    elect_commit(&B.k_empty[st]);
+                if (j + 1 == mine)
+                    elect_commit(&B.q_empty[i]);
+            }
+            t += (uint32_t)n;
+        }
+        finish();
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- P.V
+        const uint64_t vdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kValuesAt, kBox, 1024, 2);  // N-major value boxes
+        uint32_t t = 0;                                  // value tiles of the items before
+        uint32_t ppar = 0;                               // phase bit i: probabilities of query tile i
+        for (int w; ok && (w = next_item()) >= 0;) {
+            int n0, n1, nk;
             {
                 const Item it = get_item(a, ntiles, w);
                 n0 = __shfl_sync(0xffffffffu, it.n0, 0);
@@ -475,26 +494,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nk = __shfl_sync(0xffffffffu, it.t.nk, 0);
             }
             const int n = max(n0, n1);
-            // per key tile and query tile: P.V of this tile, scores of the next
+            // the first to store probabilities waits for all items before
+            if (n > 0)
+                elect_commit(&B.p_free[n0 > 0 ? 0 : 1]);
 #pragma unroll 1
-            for (int x = -2; ok && x < 2 * n; ++x) {
+            for (int x = 0; x < 2 * n; ++x) {
                 const int j = x >> 1, i = x & 1;
                 const int mine = i ? n1 : n0, other = i ? n0 : n1;
-                // the first query tile with keys in a tile waits for its boxes, the last one frees them
-                if (j >= 0 && j < mine)
-                    issue_pv(i, j, i == 0 || j >= other, i == 1 || j >= other);
-                if (ok && j + 1 < mine)
-                    issue_s(i, j + 1, i == 0 || j + 1 >= other, i == 1 || j + 1 >= other);
+                if (j >= mine)
+                    continue;
+                const uint32_t st = (t + j) & 1;
+                bool in = true;
+                if (i == 0 || j >= other) {              // the first of the tile's uses
+                    in = mbar_wait(&B.v_full[st], ((t + j) >> 1) & 1);
+                    // value rows past the sequence are zeroed: their
+                    // probabilities are 0, and 0 * NaN would poison the output
+                    const int ntok = nk - j * kKeys;
+                    if (ntok < kKeys) {
+                        in = __all_sync(0xffffffffu, in);
+                        unsigned char *v0 = smem + Lay::kValuesAt + st * Lay::kValueTile;
+                        for (int idx = lane; in && idx < (kKeys - ntok) * 8 * NVB; idx += 32) {
+                            const int b = idx / ((kKeys - ntok) * 8), rem = idx % ((kKeys - ntok) * 8);
+                            *reinterpret_cast<uint4 *>(v0 + b * kBox + (ntok + rem / 8) * 128 + (rem % 8) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                in = in && mbar_wait(&B.p_full[i], (ppar >> i) & 1);
+                ppar ^= 1u << i;
+                ok = __all_sync(0xffffffffu, in);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t vd = vdesc + (uint64_t)(st * (Lay::kValueTile >> 4));
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    elect_ts(tO + i * kTile, tP + 8 * k, vd + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+                // who is next to store probabilities: the other query tile
+                // where it has this tile (1) or the next one (0) to work off,
+                // else this one while it has more; after the item's last, see
+                // the item's start
+                const int next = j + i < other ? i ^ 1 : j + 1 < mine ? i : -1;
+                if (next >= 0)
+                    elect_commit(&B.p_free[next]);
+                if (i == 1 || j >= other)                // the last of the tile's uses
+                    elect_commit(&B.v_empty[st]);
+                if (j + 1 == mine)
+                    elect_commit(&B.o_full[i]);
             }
-            base += (uint32_t)n * Lay::kStep;
+            t += (uint32_t)n;
         }
-        if (!ok && lane == 0 && a.err)
-            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
-        // every MMA this thread issued has completed before TMEM is freed
-        elect_commit(&B.mma_done);
-        if (!mbar_wait(&B.mma_done, 0) && lane == 0 && a.err)
-            atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
-        __syncwarp();
+        finish();
     }
     } else {
         set_regs_up<kSoftmaxRegs>();
@@ -503,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3;
         const int row = i * kTile + quarter * 32 + lane; // of the item
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        const uint32_t s_addr = tS + i * kTile + lane_addr, o_addr = tO + i * kTile + lane_addr;
+        const uint32_t s_addr = tS + i * kKeys + lane_addr, o_addr = tO + i * kTile + lane_addr;
+        const uint32_t p_addr = tP + lane_addr;
         const float c = a.scale_log2;
         uint32_t sn = 0, on = 0;                         // score tiles and outputs taken
         for (int w; ok && (w = next_item()) >= 0;) {
@@ -515,36 +568,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int lim_first = __shfl_sync(0xffffffffu, lim, 0);     // limits grow with the row
             float m_ref = -INFINITY, l = 0.f;
+            const float none = c >= 0.f ? -INFINITY : INFINITY;
             for (int j = 0; j < n; ++j) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&B.s_full[i], sn & 1));
                 if (!ok)
                     break;
                 ++sn;
                 tc_fence_after();
-                float s[kTile];
+                const int nvalid = lim - j * kKeys;
+                const bool partial = lim_first - j * kKeys < kKeys;
+                // the next third is on its way while a third's maximum is taken
+                float s[kKeys];
+                float mx[3];
+                tmem_ld32_start(s_addr, s);
 #pragma unroll
-                for (int x = 0; x < kTile; x += 32)
-                    tmem_ld32_start(s_addr + x, s + x);
-#pragma unroll
-                for (int x = 0; x < kTile; x += 32)
+                for (int x = 0; x < kKeys; x += 32) {
                     tmem_ld_wait(s + x);
-                // raw scores: the scale is folded into the exponent's FMA; for
-                // a negative scale the row's maximum is at the lowest score
-                const int nvalid = lim - j * kTile;
-                if (lim_first - j * kTile < kTile) {
-                    const float none = c >= 0.f ? -INFINITY : INFINITY;
+                    if (x + 32 < kKeys) {
+                        tmem_ld32_start(s_addr + x + 32, s + x + 32);
+                    } else {
+                        // the scores are in registers: the next ones may come
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&B.s_free[i]);
+                    }
+                    // raw scores: the scale is folded into the exponent's FMA;
+                    // for a negative scale the row's maximum is at the lowest
+                    if (partial) {
 #pragma unroll
-                    for (int x = 0; x < kTile; ++x)
-                        s[x] = x < nvalid ? s[x] : none;
+                        for (int y = x; y < x + 32; ++y)
+                            s[y] = y < nvalid ? s[y] : none;
+                    }
+                    if (c >= 0.f)
+                        mx[x / 32] = reduce_extreme<true, 32>(s + x);
+                    else
+                        mx[x / 32] = -reduce_extreme<false, 32>(s + x);
                 }
-                float mt;
-                if (c >= 0.f) {
-                    const float e = reduce_extreme<true, kTile>(s);
-                    mt = e == -INFINITY ? -INFINITY : c * e;
-                } else {
-                    const float e = reduce_extreme<false, kTile>(s);
-                    mt = e == INFINITY ? -INFINITY : c * e;
-                }
+                const float e = latent::fmax3(mx[0], mx[1], mx[2]);
+                const float mt = e == -INFINITY ? -INFINITY : fabsf(c) * e;
                 float alpha = 1.f;
                 bool rescale = false;
                 if (mt > m_ref + kRescaleThreshold) {
@@ -557,24 +619,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                 float sx[4] = {0.f, 0.f, 0.f, 0.f}, sy[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int y = 0; y < kTile; y += 32) {
-                    uint32_t pk[16];
+                uint32_t pk[kKeys / 2];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
+                for (int x = 0; x < kKeys / 2; ++x) {
+                    {
                         float x0, x1;
-                        ffma2(x0, x1, s[y + 2 * x], s[y + 2 * x + 1], c, c, nm, nm);
-                        const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
+                        ffma2(x0, x1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
+                        float e0, e1;
+                        if (x % kExpCycle >= kExpCycle - kExpFma) {
+                            exp2_fma(e0, e1, x0, x1);
+                        } else {
+                            e0 = exp2_approx(x0);
+                            e1 = exp2_approx(x1);
+                        }
                         fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
                         const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
                         pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
                     }
-                    tmem_st16_start(s_addr + y / 2, pk);
                 }
-                l = l * alpha + (((sx[0] + sy[0]) + (sx[1] + sy[1])) + ((sx[2] + sy[2]) + (sx[3] + sy[3])));
-                tmem_st_wait();
-                // the scores' commit covers every earlier P.V, so the output
-                // holds all tiles before this one; TMEM accesses are
-                // warp-wide: the warp's rows are rescaled when any needs it
+                // the probabilities' columns are free, and the output holds all
+                // tiles before this one, when every P.V before this tile's is
+                // done; TMEM accesses are warp-wide: the warp's rows are
+                // rescaled when any needs it
+                ok = __all_sync(0xffffffffu, mbar_wait(&B.p_free[i], (sn - 1) & 1));
+                if (!ok)
+                    break;
+                tc_fence_after();
                 if (__any_sync(0xffffffffu, rescale)) {
                     uint32_t r[32];
 #pragma unroll 1
@@ -586,8 +656,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st32(o_addr + 32 * x, r);
                     }
                 }
+#pragma unroll
+                for (int x = 0; x < kKeys / 2; x += 16)
+                    tmem_st16_start(p_addr + x, pk + x);
+                tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&B.p_full[i]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&B.p_full[i]);
+                l = l * alpha + (((sx[0] + sy[0]) + (sx[1] + sy[1])) + ((sx[2] + sy[2]) + (sx[3] + sy[3])));
             }
             if (!ok)
                 break;
@@ -699,12 +776,12 @@ bool strides(const int64_t *given, long long token, long long head, long long *o
     return true;
 }
 
-// Tensor map of x [tokens][heads][d] in boxes of 128 tokens x 64 columns (zeros past d and past the last token).
-bool rows_map(CUtensorMap *map, const void *x, int d, int heads, long long tokens, const long long *st)
+// Tensor map of x [tokens][heads][d] in boxes of `rows` tokens x 64 columns (zeros past d and past the last token).
+bool rows_map(CUtensorMap *map, const void *x, int d, int heads, long long tokens, const long long *st, int rows)
 {
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t bytes[2] = {(cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
-    const cuuint32_t box[3] = {64, 1, kTile};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, bytes, box,
                         CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
@@ -776,13 +853,13 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     Maps &m = c.maps;
     // without keys there is nothing to load: the maps only have to be well formed
     const long long rows = tk > 0 ? tk : 1;
-    bool fine = rows_map(&m.q, q_nope, p->d_nope, (int)H, tq, sq) && rows_map(&m.k, k_nope, p->d_nope, (int)KH, rows, sk) &&
-                rows_map(&m.v, v, p->d_v, (int)KH, rows, sv);
+    bool fine = rows_map(&m.q, q_nope, p->d_nope, (int)H, tq, sq, kTile) && rows_map(&m.k, k_nope, p->d_nope, (int)KH, rows, sk, kKeys) &&
+                rows_map(&m.v, v, p->d_v, (int)KH, rows, sv, kKeys);
     if (fine && p->d_rope > 0) {
-        fine = rows_map(&m.qr, q_rope, p->d_rope, (int)H, tq, sqr);
+        fine = rows_map(&m.qr, q_rope, p->d_rope, (int)H, tq, sqr, kTile);
         const cuuint64_t dims[2] = {(cuuint64_t)p->d_rope, (cuuint64_t)rows};
         const cuuint64_t bytes[1] = {(cuuint64_t)skr[0] * 2};
-        const cuuint32_t box[2] = {64, kTile};
+        const cuuint32_t box[2] = {64, kKeys};
         fine = fine && encode_tiled(&m.kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(k_rope), dims, bytes,
                                     box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
     } else {
