@@ -9,10 +9,15 @@
 // head against 2 (576 + 512); expanding a token costs 2 * 512 * 256 a head, so
 // the expanded form does less work from about 170 new tokens on.
 //
-// A GEMM whose A rows are gathered by the block table: a tile is 128 tokens of
-// one sequence (two pages, one TMA box each), staged with the head's weights in
-// 64-wide chunks of the contraction; tcgen05 MMAs (M = 128, N = 128, K = 16)
-// accumulate keys and values side by side in TMEM.
+// A GEMM whose A rows are gathered by the block table.  A tile is 128 tokens of
+// one sequence (two pages, one TMA box each) with all of its group's latent
+// columns in shared memory; the weights of two heads at a time stream past it
+// in 64-wide chunks of the contraction, first both W_UK, then both W_UV, as
+// tcgen05 MMAs of 128 x 256 x 16 into one of two TMEM accumulators, so that
+// one is stored while the other fills.  Keeping the latents in place leaves 64
+// bytes a cycle and SM to read from L2 (weights only; 96 with both operands
+// streamed).  Every CTA takes the same number of (tile, group, head pair)
+// units, in order, and loads latents only where the tile or the group changes.
 #include <math.h>
 
 #include "ragged.cuh"
@@ -21,16 +26,27 @@ namespace kvattn {
 
 namespace {
 
+using ragged::elect_commit;
+using ragged::elect_ss;
+
 bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int kRows = 128;                      // tokens of a tile
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kChunk = 64;                      // contraction elements per stage
-constexpr int kBox = kRows * kChunk * 2;        // 16 KB: the tile's latents, W_UK or W_UV of one chunk
-constexpr int kStage = 3 * kBox;
-constexpr int kStages = 2;                      // 96 KB a CTA: two on an SM, one storing while the other multiplies
-constexpr uint32_t kCols = 256;                 // TMEM: 128 key and 128 value columns
-constexpr size_t kSmem = (size_t)kStages * kStage + 64;
+constexpr int kBox = kRows * kChunk * 2;        // 16 KB: one chunk of the tile's latents, or of a head's weight
+constexpr int kMaxChunks = 8;                   // 512 latent columns
+constexpr int kStage = 2 * kBox;                // one chunk of two heads' weights
+constexpr int kStages = 3;
+constexpr uint32_t kCols = 256;                 // accumulator columns: 128 of each head
+
+struct Bars {
+    uint64_t a_full[kMaxChunks], a_empty;
+    uint64_t b_full[kStages], b_empty[kStages];
+    uint64_t d_full[2], d_empty[2];
+    uint64_t done;
+    uint32_t tmem_base;
+};
 
 struct ExpandArgs {
     const int32_t *header;
@@ -39,7 +55,8 @@ struct ExpandArgs {
     const __nv_bfloat16 *cache;
     __nv_bfloat16 *k, *v, *k_rope;
     int32_t *err;
-    int heads, heads_per_group, groups, d_c, d_k, d_v, d_rope, row;
+    int heads, heads_per_group, groups, pairs_per_group, d_c, d_k, d_v, d_rope, row;
+    int wide_k, wide_v;                         // outputs whose rows start on 32 bytes
     int mpps, num_pages, max_kv;
 };
 
@@ -58,153 +75,261 @@ __device__ __forceinline__ int page_or_none(const ExpandArgs &a, int seq, int pi
     return (int)page;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void store32(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// The units of this CTA, in order; every role walks them on its own.
+struct Walk {
+    int unit, end;                               // of (tile, group, head pair), pairs fastest
+    int pairs, groups;
+    int tile, group, pair;
+    __device__ __forceinline__ Walk(const ExpandArgs &a, int ntiles) : pairs(a.pairs_per_group), groups(a.groups)
+    {
+        const long long all = (long long)ntiles * groups * pairs;
+        unit = (int)(all * blockIdx.x / gridDim.x);
+        end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+        pair = unit % pairs;
+        group = unit / pairs % groups;
+        tile = unit / pairs / groups;
+    }
+    __device__ __forceinline__ bool more() const { return unit < end; }
+    // whether the unit after this one has other latents (or there is none)
+    __device__ __forceinline__ bool last_of_latents() const { return pair + 1 == pairs || unit + 1 == end; }
+    __device__ __forceinline__ void next()
+    {
+        ++unit;
+        if (++pair == pairs) {
+            pair = 0;
+            if (++group == groups) {
+                group = 0;
+                ++tile;
+            }
+        }
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const ExpandArgs a)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage);
-    uint64_t *empty = full + kStages;
-    uint64_t *done = empty + kStages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int chunks = a.d_c / kChunk;
+    unsigned char *const wts = smem + chunks * kBox;
+    Bars &B = *reinterpret_cast<Bars *>(wts + kStages * kStage);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && a.err)
             atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
         return;
     }
-    pdl_wait_primary();
-    if ((int)blockIdx.y >= a.header[0])
-        return;
-    const ragged::Tile t = a.tiles[blockIdx.y];
-    const int h = blockIdx.x, group = h / a.heads_per_group;
-    const int chunks = a.d_c / kChunk;
-    const int subs = t.nq > kPage ? 2 : 1;       // pages that hold rows of the tile
     if (threadIdx.x == 0) {
+        for (int c = 0; c < kMaxChunks; ++c)
+            mbar_init(&B.a_full[c], 1);
+        mbar_init(&B.a_empty, 1);
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&B.b_full[s], 1);
+            mbar_init(&B.b_empty[s], 1);
         }
-        mbar_init(done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.d_full[i], 1);
+            mbar_init(&B.d_empty[i], 4);
+        }
+        mbar_init(&B.done, 1);
         fence_mbar_init();
     }
     if (warp == 0)
-        tmem_alloc(tmem_slot, kCols);
+        tmem_alloc(&B.tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tacc = *tmem_slot;
+    const uint32_t tbase = B.tmem_base;
+    pdl_wait_primary();                          // the tile list
+    Walk w(a, a.header[0]);
     bool ok = true;
 
     if (warp == 0) {
+        // ---------------------------------------------------------------- TMA
         if (lane == 0) {
-            int y[2] = {0, 0};
-            for (int s = 0; s < subs; ++s)
-                y[s] = page_or_none(a, t.seq, t.tok0 / kPage + s, h == 0) * kPage;
-            int issued = 0;
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c % kStages;
-                if (c >= kStages && !mbar_wait(&empty[st], ((c / kStages) - 1) & 1)) {
-                    ok = false;
-                    break;
+            uint32_t nb = 0, na = 0;             // weight chunks, latent tiles loaded
+            bool fresh = true;
+            for (; ok && w.more(); w.next()) {
+                if (fresh) {
+                    if (na > 0 && !mbar_wait(&B.a_empty, (na - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    ++na;
+                    const ragged::Tile t = a.tiles[w.tile];
+                    const int subs = t.nq > kPage ? 2 : 1;       // pages that hold rows of the tile
+                    int y[2] = {0, 0};
+                    for (int s = 0; s < subs; ++s)
+                        y[s] = page_or_none(a, t.seq, t.tok0 / kPage + s, w.group == 0) * kPage;
+                    for (int c = 0; c < chunks; ++c) {
+                        mbar_arrive_expect_tx(&B.a_full[c], (uint32_t)(subs * (kBox / 2)));
+                        for (int s = 0; s < subs; ++s)
+                            tma_load_2d(smem + c * kBox + s * (kBox / 2), &cmap, w.group * a.d_c + c * kChunk, y[s],
+                                        &B.a_full[c]);
+                    }
                 }
-                unsigned char *base = smem + st * kStage;
-                mbar_arrive_expect_tx(&full[st], (uint32_t)(subs * (kBox / 2) + 2 * kBox));
-                for (int s = 0; s < subs; ++s)
-                    tma_load_2d(base + s * (kBox / 2), &cmap, group * a.d_c + c * kChunk, y[s], &full[st]);
-                tma_load_3d(base + kBox, &kmap, c * kChunk, 0, h, &full[st]);
-                tma_load_3d(base + 2 * kBox, &vmap, 0, c * kChunk, h, &full[st]);
-                tma_load_3d(base + 2 * kBox + kBox / 2, &vmap, 64, c * kChunk, h, &full[st]);
-                issued = c + 1;
+                fresh = w.last_of_latents();
+                const int h = w.group * a.heads_per_group + 2 * w.pair;
+                for (int kind = 0; ok && kind < 2; ++kind)
+                    for (int c = 0; c < chunks; ++c, ++nb) {
+                        const uint32_t st = nb % kStages;
+                        if (nb >= kStages && !mbar_wait(&B.b_empty[st], (nb / kStages - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        unsigned char *dst = wts + st * kStage;
+                        mbar_arrive_expect_tx(&B.b_full[st], kStage);
+                        for (int p = 0; p < 2; ++p) {
+                            if (kind == 0) {
+                                tma_load_3d(dst + p * kBox, &kmap, c * kChunk, 0, h + p, &B.b_full[st]);
+                            } else {
+                                tma_load_3d(dst + p * kBox, &vmap, 0, c * kChunk, h + p, &B.b_full[st]);
+                                tma_load_3d(dst + p * kBox + kBox / 2, &vmap, 64, c * kChunk, h + p, &B.b_full[st]);
+                            }
+                        }
+                    }
             }
             // every copy started here has landed before the CTA can exit
-            for (int st = 0; st < kStages && st < issued; ++st) {
-                const int cl = st + ((issued - 1 - st) / kStages) * kStages;
-                if (!mbar_wait(&full[st], (cl / kStages) & 1))
+            for (uint32_t s = 0; s < kStages; ++s)
+                if (nb > s && !mbar_wait(&B.b_full[s], ((nb - 1 - s) / kStages) & 1))
                     ok = false;
-            }
+            for (int c = 0; c < chunks; ++c)
+                if (na > 0 && !mbar_wait(&B.a_full[c], (na - 1) & 1))
+                    ok = false;
         }
         __syncwarp();
     } else if (warp == 1) {
-        constexpr uint32_t kidesc = idesc_bf16_f32(kRows, 128, false, false);
-        constexpr uint32_t videsc = idesc_bf16_f32(kRows, 128, false, true);
-        const uint64_t cdesc = smem_desc(smem_u32(smem), 16, 1024, 2);                    // K-major latents
-        const uint64_t kdesc = smem_desc(smem_u32(smem) + kBox, 16, 1024, 2);             // K-major rows of W_UK
-        const uint64_t vdesc = smem_desc(smem_u32(smem) + 2 * kBox, kBox / 2, 1024, 2);   // N-major rows of W_UV
-        for (int c = 0; c < chunks; ++c) {
-            const int st = c % kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (c / kStages) & 1))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t o = (uint64_t)(st * (kStage >> 4));
+        // ---------------------------------------------------------------- MMA
+        const uint64_t cdesc = smem_desc(smem_u32(smem), 16, 1024, 2);            // K-major latents
+        const uint64_t kdesc = smem_desc(smem_u32(wts), 16, 1024, 2);             // K-major rows of two W_UK
+        const uint64_t vdesc = smem_desc(smem_u32(wts), kBox / 2, 1024, 2);       // N-major rows of two W_UV
+        uint32_t nb = 0, na = 0, nd = 0;                 // weight chunks, latent tiles, accumulators
+        bool fresh = true;
+        for (; ok && w.more(); w.next()) {
+            na += fresh;
+            const bool last = w.last_of_latents();
+#pragma unroll 1
+            for (int kind = 0; ok && kind < 2; ++kind, ++nd) {
+                const uint32_t buf = nd & 1, d = tbase + buf * kCols;
+                bool in = nd < 2 || mbar_wait(&B.d_empty[buf], ((nd >> 1) - 1) & 1);
+                const uint32_t idesc = kind ? idesc_bf16_f32(kRows, kCols, false, true) : idesc_bf16_f32(kRows, kCols, false, false);
+                const uint64_t step = kind ? 128 : 2;    // sixteen rows of W_UV, sixteen columns of W_UK
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c, ++nb) {
+                    const uint32_t st = nb % kStages;
+                    if (fresh && kind == 0)
+                        in = in && mbar_wait(&B.a_full[c], (na - 1) & 1);
+                    in = in && mbar_wait(&B.b_full[st], (nb / kStages) & 1);
+                    ok = __all_sync(0xffffffffu, in);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t ad = cdesc + (uint64_t)(c * (kBox >> 4));
+                    const uint64_t bd = (kind ? vdesc : kdesc) + (uint64_t)(st * (kStage >> 4));
 #pragma unroll
-                for (int i = 0; i < kChunk / 16; ++i) {
-                    umma_ss(tacc, cdesc + o + i * 2, kdesc + o + i * 2, kidesc, (c | i) ? 1u : 0u);
-                    umma_ss(tacc + 128, cdesc + o + i * 2, vdesc + o + i * 128, videsc, (c | i) ? 1u : 0u);
+                    for (int i = 0; i < kChunk / 16; ++i)
+                        elect_ss(d, ad + i * 2, bd + i * step, idesc, (c | i) ? 1u : 0u);
+                    elect_commit(&B.b_empty[st]);
                 }
-                umma_commit(&empty[st]);
+                if (ok)
+                    elect_commit(&B.d_full[buf]);
             }
-            __syncwarp();
+            if (ok && last)
+                elect_commit(&B.a_empty);
+            fresh = last;
         }
-        if (lane == 0)
-            umma_commit(done);
-        __syncwarp();
-    } else if (h == 0) {
-        // the shared rope keys of the tile's tokens, copied once
+        // every MMA issued here has completed before TMEM is freed
+        elect_commit(&B.done);
+        ok = __all_sync(0xffffffffu, mbar_wait(&B.done, 0)) && ok;
+    } else if (warp == 2) {
+        // the shared rope keys of a tile's tokens, copied once, with its first unit
         const int vecs = a.d_rope / 8;
-        for (int i = threadIdx.x - 64; i < t.nq * vecs; i += 64) {
-            const int r = i / vecs, p = i % vecs;
-            const int page = page_or_none(a, t.seq, (t.tok0 + r) / kPage, false);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (page < a.num_pages)
-                x = *reinterpret_cast<const uint4 *>(a.cache + ((long long)page * kPage + (t.tok0 + r) % kPage) * a.row +
-                                                     a.groups * a.d_c + 8 * p);
-            *reinterpret_cast<uint4 *>(a.k_rope + (long long)(t.q0 + r) * a.d_rope + 8 * p) = x;
+        for (; w.more(); w.next()) {
+            if (w.group || w.pair || !vecs)
+                continue;
+            const ragged::Tile t = a.tiles[w.tile];
+            for (int i = lane; i < t.nq * vecs; i += 32) {
+                const int r = i / vecs, p = i % vecs;
+                const int page = page_or_none(a, t.seq, (t.tok0 + r) / kPage, false);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (page < a.num_pages)
+                    x = *reinterpret_cast<const uint4 *>(
+                        a.cache + ((long long)page * kPage + (t.tok0 + r) % kPage) * a.row + a.groups * a.d_c + 8 * p);
+                *reinterpret_cast<uint4 *>(a.k_rope + (long long)(t.q0 + r) * a.d_rope + 8 * p) = x;
+            }
         }
-    }
-
-    // thread r of the CTA stores row r of the tile
-    const bool have = __all_sync(0xffffffffu, mbar_wait(done, 0));
-    tc_fence_after();
-    const int r0 = threadIdx.x;
-    const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
+    } else if (warp >= 4) {
+        // ----------------------------------------------- accumulators to memory
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const int r0 = (warp & 3) * 32 + lane;           // row of the tile
+        uint32_t nd = 0;
+        for (; ok && w.more(); w.next()) {
+            const int q0 = a.tiles[w.tile].q0, nq = a.tiles[w.tile].nq;
+            const int heads = min(2, a.heads_per_group - 2 * w.pair);
+            const int h = w.group * a.heads_per_group + 2 * w.pair;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        const int width = half ? a.d_v : a.d_k;
-        __nv_bfloat16 *out = (half ? a.v : a.k) + ((long long)h * a.max_kv + t.q0 + r0) * width;
+            for (int kind = 0; kind < 2; ++kind, ++nd) {
+                const uint32_t buf = nd & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(&B.d_full[buf], (nd >> 1) & 1));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const int width = kind ? a.d_v : a.d_k;
+                const bool wide = kind ? a.wide_v : a.wide_k;
+                __nv_bfloat16 *const rows = (kind ? a.v : a.k) + ((long long)h * a.max_kv + q0 + r0) * width;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-            if (c >= width)
-                break;
-            uint32_t r[32];
-            if (have)
-                tmem_ld32(tacc + lane_addr + 128 * half + c, r);
-            if (r0 < t.nq && have) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * j]),
-                                                                       __uint_as_float(r[8 * i + 2 * j + 1]));
-                        pk[j] = *reinterpret_cast<const uint32_t *>(&v);
+                for (int c = 0; c < 256; c += 64) {
+                    uint32_t r[64];
+                    tmem_ld64(tbase + buf * kCols + lane_addr + c, r);
+                    if (c == 192) {
+                        // the accumulator is in registers: the MMAs may have it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&B.d_empty[buf]);
                     }
-                    if (c + 8 * i < width)
-                        *reinterpret_cast<uint4 *>(out + c + 8 * i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    __nv_bfloat16 *const out = rows + (long long)(c >> 7) * a.max_kv * width + (c & 64);
+                    if (r0 < nq && (c >> 7) < heads) {
+#pragma unroll
+                        for (int i = 0; i < 64; i += 16) {
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[i + 2 * j]),
+                                                                               __uint_as_float(r[i + 2 * j + 1]));
+                                pk[j] = *reinterpret_cast<const uint32_t *>(&v);
+                            }
+                            const int col = (c & 64) + i;
+                            if (wide && col + 16 <= width) {
+                                store32(out + i, pk);
+                            } else {
+                                if (col < width)
+                                    *reinterpret_cast<uint4 *>(out + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                                if (col + 8 < width)
+                                    *reinterpret_cast<uint4 *>(out + i + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
             }
         }
     }
-    if ((!ok || !have) && lane == 0 && a.err)
+    if (!ok && lane == 0 && a.err)
         atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0)
-        tmem_dealloc(tacc, kCols);
+        tmem_dealloc(tbase, 512);
 }
 
 }  // namespace
@@ -253,7 +378,8 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     if (workspace_bytes < need)
         return KVATTN_ERR_WORKSPACE_TOO_SMALL;
     const long long cap = ragged::tile_capacity(max_kv_tokens, p->batch, kRows);
-    if (cap > 65535)
+    const int pairs = (pr.HPU + 1) / 2;
+    if (cap * pr.NU * pairs > INT32_MAX)
         return KVATTN_ERR_UNSUPPORTED;
     if (max_kv_tokens == 0)
         return KVATTN_OK;
@@ -306,6 +432,9 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.heads = pr.H;
     a.heads_per_group = pr.HPU;
     a.groups = pr.NU;
+    a.pairs_per_group = pairs;
+    a.wide_k = d_k % 16 == 0 && is_aligned(k_nope, 32);
+    a.wide_v = d_v % 16 == 0 && is_aligned(v, 32);
     a.d_c = pr.dn;
     a.d_k = d_k;
     a.d_v = d_v;
@@ -314,12 +443,14 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.mpps = pr.mpps;
     a.num_pages = pr.num_pages;
     a.max_kv = max_kv_tokens;
-    if (cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+    const size_t smem = (size_t)(pr.dn / kChunk) * kBox + kStages * kStage + sizeof(Bars);
+    if (cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return KVATTN_ERR_CUDA;
+    const long long units = cap * pr.NU * pairs, sms = sm_count();
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(pr.H, (unsigned)cap);
+    cfg.gridDim = dim3((unsigned)(units < sms ? units : sms));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

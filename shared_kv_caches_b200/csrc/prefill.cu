@@ -50,6 +50,9 @@ namespace kvattn {
 
 namespace {
 
+using ragged::elect_commit;
+using ragged::elect_ss;
+using ragged::elect_ts;
 using latent::exp2_approx;
 using latent::fadd2;
 using latent::ffma2;
@@ -140,34 +143,6 @@ __device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t *
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-
-// MMAs and commits issued by one elected lane (always the same one) in code
-// that the whole warp runs.  What the descriptors are made of is then the same
-// in every lane and stays in uniform registers: issued from a branch that only
-// lane 0 takes, every operand is moved there first, and an MMA of 64 cycles
-// took 140 to issue (clock trace of an 8K prompt); so, about 70.
-__device__ __forceinline__ void elect_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
-}
-
-__device__ __forceinline__ void elect_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
-}
-
-__device__ __forceinline__ void elect_commit(uint64_t *bar)
-{
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-                 : "memory");
 }
 
 // 32 columns; the values may be used after tmem_ld_wait, which names them.
@@ -618,24 +593,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                 float sx[4] = {0.f, 0.f, 0.f, 0.f}, sy[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
                 uint32_t pk[kKeys / 2];
 #pragma unroll
                 for (int x = 0; x < kKeys / 2; ++x) {
-                    {
-                        float x0, x1;
-                        ffma2(x0, x1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
-                        float e0, e1;
-                        if (x % kExpCycle >= kExpCycle - kExpFma) {
-                            exp2_fma(e0, e1, x0, x1);
-                        } else {
-                            e0 = exp2_approx(x0);
-                            e1 = exp2_approx(x1);
-                        }
-                        fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
-                        const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
-                        pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
+                    float x0, x1, e0, e1;
+                    ffma2(x0, x1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
+                    if (x % kExpCycle >= kExpCycle - kExpFma) {
+                        exp2_fma(e0, e1, x0, x1);
+                    } else {
+                        e0 = exp2_approx(x0);
+                        e1 = exp2_approx(x1);
                     }
+                    fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
+                    const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
+                    pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
                 }
                 // the probabilities' columns are free, and the output holds all
                 // tiles before this one, when every P.V before this tile's is
@@ -829,8 +800,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     const int st = kvattn_prefill_workspace_size(p, &need);
     if (st)
         return st;
-    if (!q_nope || !k_nope || !v || !q_start || !kv_start || !out || !workspace ||
-        (p->d_rope > 0 && (!q_rope || !k_rope)) || !isfinite(sm_scale))
+    const bool keys = p->max_kv_tokens > 0;      // without any, key and value pointers may be null
+    if (!q_nope || !q_start || !kv_start || !out || !workspace || (keys && (!k_nope || !v)) ||
+        (p->d_rope > 0 && (!q_rope || (keys && !k_rope))) || !isfinite(sm_scale))
         return KVATTN_ERR_INVALID_ARG;
     if (!is_aligned(q_nope, 16) || !is_aligned(q_rope, 16) || !is_aligned(k_nope, 16) || !is_aligned(k_rope, 16) ||
         !is_aligned(v, 16) || !is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(workspace, 256) ||
@@ -842,8 +814,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     long long sq[2], sqr[2] = {8, 8}, sk[2], sv[2], so[2];
     const int64_t kr_given[2] = {p->k_rope_stride, 8};
     long long skr[2] = {8, 8};
-    if (!strides(p->q_nope_stride, H * p->d_nope, p->d_nope, sq) || !strides(p->k_stride, p->d_nope, tk * p->d_nope, sk) ||
-        !strides(p->v_stride, p->d_v, tk * p->d_v, sv) || !strides(p->out_stride, H * p->d_v, p->d_v, so) ||
+    if (!strides(p->q_nope_stride, H * p->d_nope, p->d_nope, sq) ||
+        !strides(p->k_stride, p->d_nope, (keys ? tk : 1) * p->d_nope, sk) ||
+        !strides(p->v_stride, p->d_v, (keys ? tk : 1) * p->d_v, sv) || !strides(p->out_stride, H * p->d_v, p->d_v, so) ||
         (p->d_rope > 0 && (!strides(p->q_rope_stride, H * p->d_rope, p->d_rope, sqr) || !strides(kr_given, p->d_rope, 8, skr))))
         return KVATTN_ERR_INVALID_ARG;
     if (tq == 0)
@@ -852,7 +825,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     Call c;
     Maps &m = c.maps;
     // without keys there is nothing to load: the maps only have to be well formed
-    const long long rows = tk > 0 ? tk : 1;
+    const long long rows = keys ? tk : 1;
+    if (!keys)
+        k_nope = v = k_rope = q_nope;
     bool fine = rows_map(&m.q, q_nope, p->d_nope, (int)H, tq, sq, kTile) && rows_map(&m.k, k_nope, p->d_nope, (int)KH, rows, sk, kKeys) &&
                 rows_map(&m.v, v, p->d_v, (int)KH, rows, sv, kKeys);
     if (fine && p->d_rope > 0) {

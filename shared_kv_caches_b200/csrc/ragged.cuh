@@ -53,6 +53,34 @@ __device__ __forceinline__ int find(const int32_t *start, int n, int x)
     return lo;
 }
 
+// MMAs and commits issued by one elected lane (always the same one) in code
+// that the whole warp runs.  What the descriptors are made of is then the same
+// in every lane and stays in uniform registers: issued from a branch that only
+// lane 0 takes, every operand is moved there first, and an MMA of 64 cycles
+// took 140 to issue (clock trace of an 8K prompt); so, about 70.
+__device__ __forceinline__ void elect_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void elect_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void elect_commit(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 // One tile of a ragged batch, as the plan kernel lists them.
 struct Tile {
     int32_t q0;       // first row of the tile

@@ -329,19 +329,40 @@ def kvattn_prefill(params, q_nope, q_rope, k_nope, k_rope, v, q_start, kv_start,
                                  float(sm_scale), out, lse, workspace, int(workspace_bytes), device_error, stream)
 
 
-def _check(t, dtypes, dims, device, what):
+def _check(t, dtype, dims, device, what):
     """The tensor a helper was given: its type, its axes and its device."""
-    if t.dtype not in dtypes or t.dim() != dims or t.device != device:
-        raise ValueError(f"{what}: {dims}-d {' or '.join(str(d) for d in dtypes)} on {device} wanted, "
-                         f"got {t.dim()}-d {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.dim() != dims or t.device != device or device.type != "cuda":
+        raise ValueError(f"{what}: {dims}-d {dtype} on a CUDA device wanted ({device}), got {t.dim()}-d {t.dtype} on {t.device}")
     return t
 
 
-def _launch(device):
-    """The device's guard and its current stream (a kernel runs on the device
-    that is current when it is launched)."""
+def _dense(t, dtype, dims, device, what):
+    if not _check(t, dtype, dims, device, what).is_contiguous():
+        raise ValueError(f"{what} is not contiguous")
+    return t
+
+
+def _enqueue(what, device, fn, *args) -> None:
+    """fn(*args, stream) on the device's current stream, with that device
+    current (a kernel runs on the device that is current at its launch)."""
     import torch
-    return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    index = device.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        raise KvattnError(st, what)
+
+
+def _error_word(t, device):
+    return None if t is None else _dense(t, _torch_int32(), 1, device, "device_error").data_ptr()
+
+
+def _torch_int32():
+    import torch
+    return torch.int32
 
 
 def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_table, max_tokens, device_error=None,
@@ -352,61 +373,56 @@ def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_ta
     pos and slots.  inplace: seq_lens and free_left are cached_lens and
     free_count, updated (no new lengths are allocated)."""
     import torch
-    dev, i32 = cached_lens.device, (torch.int32,)
-    for t, dims, what in ((cached_lens, 1, "cached_lens"), (new_lens, 1, "new_lens"), (free_pages, 1, "free_pages"),
-                          (free_count, 1, "free_count"), (block_table, 2, "block_table")):
-        if not _check(t, i32, dims, dev, what).is_contiguous():
-            raise ValueError(f"{what} is not contiguous")
-    B = cached_lens.shape[0]
-    if new_lens.shape[0] != B or block_table.shape[0] != B or free_count.numel() != 1:
+    dev, i32 = cached_lens.device, torch.int32
+    _dense(cached_lens, i32, 1, dev, "cached_lens")
+    _dense(new_lens, i32, 1, dev, "new_lens")
+    _dense(free_pages, i32, 1, dev, "free_pages")
+    _dense(free_count, i32, 1, dev, "free_count")
+    _dense(block_table, i32, 2, dev, "block_table")
+    B, mpps = block_table.shape
+    n = int(max_tokens)
+    if cached_lens.shape[0] != B or new_lens.shape[0] != B or free_count.shape[0] != 1 or n < 0:
         raise ValueError("cached_lens, new_lens and block_table have one row a request, free_count one value")
-    guard, stream = _launch(dev)
-
-    def new(n):
-        return torch.empty(n, dtype=torch.int32, device=dev)
-    r = dict(block_table=block_table, seq_lens=cached_lens if inplace else new(B),
-             free_left=free_count if inplace else new(1), q_start=new(B + 1), kv_start=new(B + 1),
-             pos=new(max_tokens), slots=new(max_tokens))
-    with guard:
-        st = kvattn_build_tables(B, block_table.shape[1], free_pages.shape[0], max_tokens, _ptr(cached_lens),
-                                 _ptr(new_lens), _ptr(free_pages), _ptr(free_count), _ptr(block_table),
-                                 _ptr(r["seq_lens"]), _ptr(r["free_left"]), _ptr(r["q_start"]), _ptr(r["kv_start"]),
-                                 _ptr(r["pos"]), _ptr(r["slots"]), _ptr(device_error), stream)
-    if st:
-        raise KvattnError(st, "kvattn_build_tables")
-    return r
+    # the outputs share one allocation
+    sizes = [B + 1, B + 1, n, n] if inplace else [B + 1, B + 1, n, n, B, 1]
+    r = torch.empty(sum(sizes), dtype=i32, device=dev)
+    at = r.data_ptr()
+    ptr = [at, at + 4 * (B + 1), at + 8 * (B + 1), at + 8 * (B + 1) + 4 * n]
+    if inplace:
+        lens, left = cached_lens.data_ptr(), free_count.data_ptr()
+    else:
+        lens = ptr[3] + 4 * n
+        left = lens + 4 * B
+    _enqueue("kvattn_build_tables", dev, load().kvattn_build_tables, B, mpps, free_pages.shape[0], n,
+             cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+             block_table.data_ptr(), lens, left, *ptr, _error_word(device_error, dev))
+    v = r.split(sizes)
+    return dict(block_table=block_table, q_start=v[0], kv_start=v[1], pos=v[2], slots=v[3],
+                seq_lens=cached_lens if inplace else v[4], free_left=free_count if inplace else v[5])
 
 
 def append_slots_tensor(variant, params, new_kv, pos, slots, kv_cache, rope_base, device_error=None) -> None:
     """``kvattn_append_slots`` on tensors: new_kv bf16 [tokens][...], pos and
     slots int32 [tokens], kv_cache the pool (bf16, or e4m3 bytes)."""
     import torch
-    dev = kv_cache.device
-    _check(slots, (torch.int32,), 1, dev, "slots")
-    _check(new_kv, (torch.bfloat16,), new_kv.dim(), dev, "new_kv")
-    if pos is not None:
-        _check(pos, (torch.int32,), 1, dev, "pos")
-    n = slots.shape[0]
-    variant = int(variant)
+    dev, variant = kv_cache.device, int(variant)
+    fp8 = params.cache_dtype == KVATTN_CACHE_FP8_E4M3
+    n = _dense(slots, torch.int32, 1, dev, "slots").shape[0]
+    _dense(new_kv, torch.bfloat16, new_kv.dim(), dev, "new_kv")
+    if pos is not None and _dense(pos, torch.int32, 1, dev, "pos").shape[0] != n:
+        raise ValueError("pos has one position for each slot")
     row = params.num_kv * params.d_nope + params.d_rope
-    row *= 2 if variant in (KVATTN_GQA, KVATTN_MQA) else 1
-    if new_kv.numel() != n * row or (pos is not None and pos.shape[0] != n):
-        raise ValueError("new_kv has one row, and pos one position, for each slot")
-    if kv_cache.numel() != params.num_pages * 64 * row or kv_cache.element_size() != (
-            1 if params.cache_dtype == KVATTN_CACHE_FP8_E4M3 else 2):
+    if variant in (KVATTN_GQA, KVATTN_MQA):
+        row *= 2
+    if new_kv.numel() != n * row:
+        raise ValueError("new_kv has one row for each slot")
+    if kv_cache.numel() != params.num_pages * 64 * row or not kv_cache.is_contiguous() or (
+            kv_cache.element_size() != 1 if fp8 else kv_cache.dtype is not torch.bfloat16):
         raise ValueError("kv_cache is not the pool that params describe")
-    for t, what in ((new_kv, "new_kv"), (slots, "slots"), (kv_cache, "kv_cache")) + (
-            () if pos is None else ((pos, "pos"),)):
-        if not t.is_contiguous():
-            raise ValueError(f"{what} is not contiguous")
-    if n == 0:
-        return
-    guard, stream = _launch(dev)
-    with guard:
-        st = kvattn_append_slots(variant, params, _ptr(new_kv), n, _ptr(pos), _ptr(slots), _ptr(kv_cache), rope_base,
-                                 _ptr(device_error), stream)
-    if st:
-        raise KvattnError(st, "kvattn_append_slots")
+    if n:
+        _enqueue("kvattn_append_slots", dev, load().kvattn_append_slots, variant, ctypes.byref(params),
+                 new_kv.data_ptr(), n, None if pos is None else pos.data_ptr(), slots.data_ptr(), kv_cache.data_ptr(),
+                 rope_base, _error_word(device_error, dev))
 
 
 def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_uv, max_kv_tokens,
@@ -416,39 +432,30 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
     [H][max_kv_tokens][d_v] and k_rope [max_kv_tokens][d_rope] (None without a
     rope part)."""
     import torch
-    dev, bf16 = kv_cache.device, (torch.bfloat16,)
+    dev, bf16 = kv_cache.device, torch.bfloat16
     H, dn, dr, n = params.num_q_heads, params.d_nope, params.d_rope, int(max_kv_tokens)
-    _check(kv_cache, bf16, kv_cache.dim(), dev, "kv_cache")
-    _check(w_uk, bf16, 3, dev, "w_uk")
-    _check(w_uv, bf16, 3, dev, "w_uv")
-    _check(kv_start, (torch.int32,), 1, dev, "kv_start")
+    _dense(kv_cache, bf16, kv_cache.dim(), dev, "kv_cache")
+    _dense(w_uk, bf16, 3, dev, "w_uk")
+    _dense(w_uv, bf16, 3, dev, "w_uv")
+    _dense(kv_start, torch.int32, 1, dev, "kv_start")
     d_k, d_v = w_uk.shape[1], w_uv.shape[2]
     if w_uk.shape != (H, d_k, dn) or w_uv.shape != (H, dn, d_v) or kv_start.shape[0] != params.batch + 1:
         raise ValueError("w_uk is [H][d_k][d_nope], w_uv [H][d_nope][d_v], kv_start [batch + 1]")
     if kv_cache.numel() != params.num_pages * 64 * (params.num_kv * dn + dr):
         raise ValueError("kv_cache is not the pool that params describe")
-    if block_table is not None and _check(block_table, (torch.int32,), 2, dev, "block_table").shape != (
+    if block_table is not None and _dense(block_table, torch.int32, 2, dev, "block_table").shape != (
             params.batch, params.max_pages_per_seq):
         raise ValueError("block_table is [batch][max_pages_per_seq]")
-    for t, what in ((kv_cache, "kv_cache"), (w_uk, "w_uk"), (w_uv, "w_uv"), (kv_start, "kv_start")) + (
-            () if block_table is None else ((block_table, "block_table"),)):
-        if not t.is_contiguous():
-            raise ValueError(f"{what} is not contiguous")
-
-    def new(*shape):
-        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    r = dict(k=new(H, n, d_k), v=new(H, n, d_v), k_rope=new(n, dr) if dr else None)
-    ws = torch.empty(kvattn_expand_workspace_size(variant, params, n), dtype=torch.uint8, device=dev)
-    if n == 0:
-        return r
-    guard, stream = _launch(dev)
-    with guard:
-        st = kvattn_expand_kv(variant, params, _ptr(kv_cache), _ptr(block_table), _ptr(kv_start), n, d_k, d_v,
-                              _ptr(w_uk), _ptr(w_uv), _ptr(r["k"]), _ptr(r["v"]), _ptr(r["k_rope"]), _ptr(ws),
-                              ws.numel(), _ptr(device_error), stream)
-    if st:
-        raise KvattnError(st, "kvattn_expand_kv")
-    return r
+    k = torch.empty((H, n, d_k), dtype=bf16, device=dev)
+    v = torch.empty((H, n, d_v), dtype=bf16, device=dev)
+    k_rope = torch.empty((n, dr), dtype=bf16, device=dev) if dr else None
+    if n:
+        ws = torch.empty(kvattn_expand_workspace_size(variant, params, n), dtype=torch.uint8, device=dev)
+        _enqueue("kvattn_expand_kv", dev, load().kvattn_expand_kv, int(variant), ctypes.byref(params),
+                 kv_cache.data_ptr(), _ptr(block_table), kv_start.data_ptr(), n, d_k, d_v, w_uk.data_ptr(),
+                 w_uv.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_rope), ws.data_ptr(), ws.numel(),
+                 _error_word(device_error, dev))
+    return dict(k=k, v=v, k_rope=k_rope)
 
 
 def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, causal=True, out=None, lse=None,
@@ -460,43 +467,39 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
     [B + 1].  Returns out [T][H][d_v] and lse [T][H]; rows past the last
     sequence are left as they were."""
     import torch
-    dev, bf16 = q_nope.device, (torch.bfloat16,)
+    dev, bf16 = q_nope.device, torch.bfloat16
+    rope = q_rope is not None
+    if rope != (k_rope is not None):
+        raise ValueError("q_rope and k_rope go together")
     for t, dims, what in ((q_nope, 3, "q_nope"), (k, 3, "k"), (v, 3, "v")) + (
-            () if q_rope is None else ((q_rope, 3, "q_rope"), (k_rope, 2, "k_rope"))):
-        if _check(t, bf16, dims, dev, what).shape[-1] > 1 and t.stride(-1) != 1:
+            ((q_rope, 3, "q_rope"), (k_rope, 2, "k_rope")) if rope else ()):
+        if _check(t, bf16, dims, dev, what).stride(-1) != 1:
             raise ValueError(f"{what}: the last axis is not contiguous")
-    for t, what in ((q_start, "q_start"), (kv_start, "kv_start")):
-        if not _check(t, (torch.int32,), 1, dev, what).is_contiguous():
-            raise ValueError(f"{what} is not contiguous")
-    (T, H, dn), (KH, Tk, d_v), B = q_nope.shape, v.shape, q_start.shape[0] - 1
-    dr = 0 if q_rope is None else q_rope.shape[2]
+    B = _dense(q_start, torch.int32, 1, dev, "q_start").shape[0] - 1
+    _dense(kv_start, torch.int32, 1, dev, "kv_start")
+    (T, H, dn), (KH, Tk, d_v) = q_nope.shape, v.shape
+    dr = q_rope.shape[2] if rope else 0
     if k.shape != (KH, Tk, dn) or kv_start.shape[0] != B + 1 or (
-            dr and (q_rope.shape != (T, H, dr) or k_rope.shape != (Tk, dr))) or (q_rope is None) != (k_rope is None):
+            rope and (q_rope.shape != (T, H, dr) or k_rope.shape != (Tk, dr))):
         raise ValueError("the shapes of queries, keys, values and starts do not fit together")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=dev)
-    elif _check(out, (torch.bfloat16, torch.float32), 3, dev, "out").shape != (T, H, d_v) or out.stride(-1) != 1:
+        out = torch.empty((T, H, d_v), dtype=torch.float32 if out_fp32 else bf16, device=dev)
+    elif _check(out, torch.float32 if out_fp32 else bf16, 3, dev, "out").shape != (T, H, d_v) or out.stride(-1) != 1:
         raise ValueError("out is [T][H][d_v] with a contiguous last axis")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    elif _check(lse, (torch.float32,), 2, dev, "lse").shape != (T, H) or not lse.is_contiguous():
+    elif _dense(lse, torch.float32, 2, dev, "lse").shape != (T, H):
         raise ValueError("lse is [T][H]")
-    r = dict(out=out, lse=lse)
-    if T == 0:
-        return r
-
-    def steps(t, token, head):
-        return (ctypes.c_int64 * 2)(t.stride(token), t.stride(head))
-    p = kvattn_prefill_params(B, H, KH, dn, dr, d_v, T, Tk, 1 if causal else 0,
-                              KVATTN_OUT_FP32 if out.dtype == torch.float32 else KVATTN_OUT_BF16, steps(q_nope, 0, 1),
-                              steps(q_rope, 0, 1) if dr else steps(q_nope, 0, 1), steps(k, 1, 0), steps(v, 1, 0),
-                              steps(out, 0, 1), k_rope.stride(0) if dr else 0)
-    ws = torch.empty(kvattn_prefill_workspace_size(p), dtype=torch.uint8, device=dev)
-    guard, stream = _launch(dev)
-    with guard:
-        st = kvattn_prefill(p, _ptr(q_nope), _ptr(q_rope), _ptr(k), _ptr(k_rope), _ptr(v), _ptr(q_start),
-                            _ptr(kv_start), sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _ptr(device_error),
-                            stream)
-    if st:
-        raise KvattnError(st, "kvattn_prefill")
-    return r
+    if T:
+        def steps(t, token=0, head=1):
+            # an axis of one element has no stride of its own
+            return (t.stride(token) if t.shape[token] > 1 else 0, t.stride(head) if t.shape[head] > 1 else 0)
+        p = kvattn_prefill_params(B, H, KH, dn, dr, d_v, T, Tk, 1 if causal else 0,
+                                  KVATTN_OUT_FP32 if out_fp32 else KVATTN_OUT_BF16, steps(q_nope),
+                                  steps(q_rope) if rope else (0, 0), steps(k, 1, 0), steps(v, 1, 0), steps(out),
+                                  k_rope.stride(0) if rope and Tk > 1 else 0)
+        ws = torch.empty(kvattn_prefill_workspace_size(p), dtype=torch.uint8, device=dev)
+        _enqueue("kvattn_prefill", dev, load().kvattn_prefill, ctypes.byref(p), q_nope.data_ptr(), _ptr(q_rope),
+                 k.data_ptr(), _ptr(k_rope), v.data_ptr(), q_start.data_ptr(), kv_start.data_ptr(), sm_scale,
+                 out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _error_word(device_error, dev))
+    return dict(out=out, lse=lse)
