@@ -10,14 +10,18 @@
 // the expanded form does less work from about 170 new tokens on.
 //
 // A GEMM whose A rows are gathered by the block table.  A tile is 128 tokens of
-// one sequence (two pages, one TMA box each) with all of its group's latent
-// columns in shared memory; the weights of two heads at a time stream past it
-// in 64-wide chunks of the contraction, first both W_UK, then both W_UV, as
-// tcgen05 MMAs of 128 x 256 x 16 into one of two TMEM accumulators, so that
-// one is stored while the other fills.  Keeping the latents in place leaves 64
-// bytes a cycle and SM to read from L2 (weights only; 96 with both operands
-// streamed).  Every CTA takes the same number of (tile, group, head pair)
-// units, in order, and loads latents only where the tile or the group changes.
+// one sequence (two pages, one TMA box each).  Two CTAs of a cluster work on
+// two tiles and two heads: each keeps all of its own tile's latent columns in
+// shared memory and streams its own head's weights past them in 64-wide chunks
+// of the contraction, first W_UK, then W_UV; tcgen05 MMAs of the pair
+// (cta_group::2, 256 x 256 x 16) multiply both tiles with both heads, into one
+// of two TMEM accumulators, so that one is stored while the other fills.  With
+// latents in place and a head's weights read once for two tiles, an SM reads
+// 32 bytes a cycle from L2 while its MMAs run; one CTA on its own needs 64, and
+// the 96 KB that it can have in flight are then no more than the latency
+// times that (818 against ... us).  Every cluster takes the same number of
+// (tile pair, group, head pair) units, in order, and loads latents only where
+// the tiles or the group change.
 #include <math.h>
 
 #include "ragged.cuh"
@@ -26,9 +30,6 @@ namespace kvattn {
 
 namespace {
 
-using ragged::elect_commit;
-using ragged::elect_ss;
-
 bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int kRows = 128;                      // tokens of a tile
@@ -36,17 +37,77 @@ constexpr int kThreads = 256;
 constexpr int kChunk = 64;                      // contraction elements per stage
 constexpr int kBox = kRows * kChunk * 2;        // 16 KB: one chunk of the tile's latents, or of a head's weight
 constexpr int kMaxChunks = 8;                   // 512 latent columns
-constexpr int kStage = 2 * kBox;                // one chunk of two heads' weights
-constexpr int kStages = 3;
+constexpr int kMaxStages = 8;                   // as many 16 KB stages as fit beside the latents
+constexpr int kOutBox = 32 * 128;               // 32 rows x 64 columns on their way out, two for each storing warp
+constexpr int kOutBytes = 4 * 2 * kOutBox;
+constexpr int kSmemMax = 227 * 1024;
 constexpr uint32_t kCols = 256;                 // accumulator columns: 128 of each head
 
+// The barriers that the MMAs wait on are the leader's (rank 0): both CTAs' TMA
+// loads count on them.  The others are each CTA's own, arrived on by commits
+// that go to both.
 struct Bars {
     uint64_t a_full[kMaxChunks], a_empty;
-    uint64_t b_full[kStages], b_empty[kStages];
+    uint64_t b_full[kMaxStages], b_empty[kMaxStages];
     uint64_t d_full[2], d_empty[2];
     uint64_t done;
     uint32_t tmem_base;
 };
+
+constexpr int stages_of(int chunks)
+{
+    const int fit = (kSmemMax - (int)sizeof(Bars) - kOutBytes) / kBox - chunks;
+    return fit < kMaxStages ? fit : kMaxStages;
+}
+
+// The pair's forms of the tcgen05 instructions (both CTAs allocate and free).
+__device__ __forceinline__ void tmem_alloc2(uint32_t *dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void elect_ss2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+// Arrive on the barrier at this place in both CTAs once the MMAs so far are done.
+__device__ __forceinline__ void elect_commit2(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+                 "%1;\n\t}" ::"r"(smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// TMA loads into this CTA's shared memory that count on a barrier of the
+// leader (bar: its shared::cluster address).
+__device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+                 "{%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+                 "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
 
 struct ExpandArgs {
     const int32_t *header;
@@ -56,7 +117,6 @@ struct ExpandArgs {
     __nv_bfloat16 *k, *v, *k_rope;
     int32_t *err;
     int heads, heads_per_group, groups, pairs_per_group, d_c, d_k, d_v, d_rope, row;
-    int wide_k, wide_v;                         // outputs whose rows start on 32 bytes
     int mpps, num_pages, max_kv;
 };
 
@@ -75,26 +135,35 @@ __device__ __forceinline__ int page_or_none(const ExpandArgs &a, int seq, int pi
     return (int)page;
 }
 
-__device__ __forceinline__ void store32(void *p, const uint32_t *r)
+// TMA store of a box from shared memory, and the groups that such stores are
+// waited for in.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, const void *src)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
                  : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// The units of this CTA, in order; every role walks them on its own.
+// All but the last group have been read from shared memory.
+__device__ __forceinline__ void tma_store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// The units of this cluster, in order; every role walks them on its own.
 struct Walk {
-    int unit, end;                               // of (tile, group, head pair), pairs fastest
+    int unit, end;                               // of (tile pair, group, head pair), heads fastest
     int pairs, groups;
-    int tile, group, pair;
+    int tiles, group, pair;
     __device__ __forceinline__ Walk(const ExpandArgs &a, int ntiles) : pairs(a.pairs_per_group), groups(a.groups)
     {
-        const long long all = (long long)ntiles * groups * pairs;
-        unit = (int)(all * blockIdx.x / gridDim.x);
-        end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+        const long long all = (long long)((ntiles + 1) / 2) * groups * pairs;
+        const unsigned c = blockIdx.x / 2, n = gridDim.x / 2;
+        unit = (int)(all * c / n);
+        end = (int)(all * (c + 1) / n);
         pair = unit % pairs;
         group = unit / pairs % groups;
-        tile = unit / pairs / groups;
+        tiles = unit / pairs / groups;
     }
     __device__ __forceinline__ bool more() const { return unit < end; }
     // whether the unit after this one has other latents (or there is none)
@@ -106,20 +175,35 @@ struct Walk {
             pair = 0;
             if (++group == groups) {
                 group = 0;
-                ++tile;
+                ++tiles;
             }
         }
     }
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+// The tile of CTA `rank` in the walk's tile pair (no rows where the list ends).
+__device__ __forceinline__ ragged::Tile pair_tile(const ExpandArgs &a, const Walk &w, int ntiles, int rank)
+{
+    const int i = 2 * w.tiles + rank;
+    ragged::Tile t = a.tiles[min(i, ntiles - 1)];
+    if (i >= ntiles)
+        t.nq = 0;
+    return t;
+}
+
+__device__ __forceinline__ int pages_in(const ragged::Tile &t) { return (t.nq + kPage - 1) / kPage; }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap, const ExpandArgs a)
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kout,
+                  const __grid_constant__ CUtensorMap vout, const ExpandArgs a)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
-    const int chunks = a.d_c / kChunk;
+    const int chunks = a.d_c / kChunk, stages = stages_of(chunks);
     unsigned char *const wts = smem + chunks * kBox;
-    Bars &B = *reinterpret_cast<Bars *>(wts + kStages * kStage);
+    unsigned char *const outs = wts + stages * kBox;
+    Bars &B = *reinterpret_cast<Bars *>(outs + kOutBytes);
+    const int rank = (int)cluster_ctarank();
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && a.err)
@@ -130,25 +214,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kMaxChunks; ++c)
             mbar_init(&B.a_full[c], 1);
         mbar_init(&B.a_empty, 1);
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&B.b_full[s], 1);
             mbar_init(&B.b_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&B.d_full[i], 1);
-            mbar_init(&B.d_empty[i], 4);
+            mbar_init(&B.d_empty[i], 8);
         }
         mbar_init(&B.done, 1);
         fence_mbar_init();
     }
     if (warp == 0)
-        tmem_alloc(&B.tmem_base, 512);
+        tmem_alloc2(&B.tmem_base, 512);
     tc_fence_before();
-    __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tbase = B.tmem_base;
     pdl_wait_primary();                          // the tile list
-    Walk w(a, a.header[0]);
+    const int ntiles = a.header[0];
+    Walk w(a, ntiles);
     bool ok = true;
 
     if (warp == 0) {
@@ -163,90 +248,96 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     ++na;
-                    const ragged::Tile t = a.tiles[w.tile];
-                    const int subs = t.nq > kPage ? 2 : 1;       // pages that hold rows of the tile
+                    const ragged::Tile t = pair_tile(a, w, ntiles, rank);
+                    const int subs = pages_in(t), both = subs + pages_in(pair_tile(a, w, ntiles, rank ^ 1));
                     int y[2] = {0, 0};
                     for (int s = 0; s < subs; ++s)
                         y[s] = page_or_none(a, t.seq, t.tok0 / kPage + s, w.group == 0) * kPage;
                     for (int c = 0; c < chunks; ++c) {
-                        mbar_arrive_expect_tx(&B.a_full[c], (uint32_t)(subs * (kBox / 2)));
+                        const uint32_t bar = mapa_shared(smem_u32(&B.a_full[c]), 0);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&B.a_full[c], (uint32_t)(both * (kBox / 2)));
                         for (int s = 0; s < subs; ++s)
-                            tma_load_2d(smem + c * kBox + s * (kBox / 2), &cmap, w.group * a.d_c + c * kChunk, y[s],
-                                        &B.a_full[c]);
+                            pair_load_2d(smem + c * kBox + s * (kBox / 2), &cmap, w.group * a.d_c + c * kChunk, y[s], bar);
                     }
                 }
                 fresh = w.last_of_latents();
-                const int h = w.group * a.heads_per_group + 2 * w.pair;
+                const int h = w.group * a.heads_per_group + 2 * w.pair + rank;
                 for (int kind = 0; ok && kind < 2; ++kind)
                     for (int c = 0; c < chunks; ++c, ++nb) {
-                        const uint32_t st = nb % kStages;
-                        if (nb >= kStages && !mbar_wait(&B.b_empty[st], (nb / kStages - 1) & 1)) {
+                        const uint32_t st = nb % stages;
+                        if (nb >= (uint32_t)stages && !mbar_wait(&B.b_empty[st], (nb / stages - 1) & 1)) {
                             ok = false;
                             break;
                         }
-                        unsigned char *dst = wts + st * kStage;
-                        mbar_arrive_expect_tx(&B.b_full[st], kStage);
-                        for (int p = 0; p < 2; ++p) {
-                            if (kind == 0) {
-                                tma_load_3d(dst + p * kBox, &kmap, c * kChunk, 0, h + p, &B.b_full[st]);
-                            } else {
-                                tma_load_3d(dst + p * kBox, &vmap, 0, c * kChunk, h + p, &B.b_full[st]);
-                                tma_load_3d(dst + p * kBox + kBox / 2, &vmap, 64, c * kChunk, h + p, &B.b_full[st]);
-                            }
+                        unsigned char *dst = wts + st * kBox;
+                        const uint32_t bar = mapa_shared(smem_u32(&B.b_full[st]), 0);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&B.b_full[st], 2 * kBox);
+                        if (kind == 0) {
+                            pair_load_3d(dst, &kmap, c * kChunk, 0, h, bar);
+                        } else {
+                            pair_load_3d(dst, &vmap, 0, c * kChunk, h, bar);
+                            pair_load_3d(dst + kBox / 2, &vmap, 64, c * kChunk, h, bar);
                         }
                     }
             }
-            // every copy started here has landed before the CTA can exit
-            for (uint32_t s = 0; s < kStages; ++s)
-                if (nb > s && !mbar_wait(&B.b_full[s], ((nb - 1 - s) / kStages) & 1))
-                    ok = false;
-            for (int c = 0; c < chunks; ++c)
-                if (na > 0 && !mbar_wait(&B.a_full[c], (na - 1) & 1))
-                    ok = false;
+            // every copy that counts on the leader's barriers has landed before
+            // it comes to the cluster's last barrier, and so before either exits
+            if (rank == 0) {
+                for (uint32_t s = 0; s < (uint32_t)stages; ++s)
+                    if (nb > s && !mbar_wait(&B.b_full[s], ((nb - 1 - s) / stages) & 1))
+                        ok = false;
+                for (int c = 0; c < chunks; ++c)
+                    if (na > 0 && !mbar_wait(&B.a_full[c], (na - 1) & 1))
+                        ok = false;
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA
+        // ------------------------------------------------- MMA (of the leader)
         const uint64_t cdesc = smem_desc(smem_u32(smem), 16, 1024, 2);            // K-major latents
-        const uint64_t kdesc = smem_desc(smem_u32(wts), 16, 1024, 2);             // K-major rows of two W_UK
-        const uint64_t vdesc = smem_desc(smem_u32(wts), kBox / 2, 1024, 2);       // N-major rows of two W_UV
+        const uint64_t kdesc = smem_desc(smem_u32(wts), 16, 1024, 2);             // K-major rows of W_UK
+        const uint64_t vdesc = smem_desc(smem_u32(wts), kBox / 2, 1024, 2);       // N-major rows of W_UV
         uint32_t nb = 0, na = 0, nd = 0;                 // weight chunks, latent tiles, accumulators
         bool fresh = true;
-        for (; ok && w.more(); w.next()) {
+        for (; ok && rank == 0 && w.more(); w.next()) {
             na += fresh;
             const bool last = w.last_of_latents();
 #pragma unroll 1
             for (int kind = 0; ok && kind < 2; ++kind, ++nd) {
                 const uint32_t buf = nd & 1, d = tbase + buf * kCols;
-                bool in = nd < 2 || mbar_wait(&B.d_empty[buf], ((nd >> 1) - 1) & 1);
-                const uint32_t idesc = kind ? idesc_bf16_f32(kRows, kCols, false, true) : idesc_bf16_f32(kRows, kCols, false, false);
+                bool in = nd < 2 || mbar_wait_cluster(&B.d_empty[buf], ((nd >> 1) - 1) & 1);
+                const uint32_t idesc = idesc_bf16_f32(2 * kRows, kCols, false, false) | (kind ? 1u << 16 : 0u);   // N-major W_UV
                 const uint64_t step = kind ? 128 : 2;    // sixteen rows of W_UV, sixteen columns of W_UK
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c, ++nb) {
-                    const uint32_t st = nb % kStages;
+                    const uint32_t st = nb % stages;
                     if (fresh && kind == 0)
                         in = in && mbar_wait(&B.a_full[c], (na - 1) & 1);
-                    in = in && mbar_wait(&B.b_full[st], (nb / kStages) & 1);
+                    in = in && mbar_wait(&B.b_full[st], (nb / stages) & 1);
                     ok = __all_sync(0xffffffffu, in);
                     if (!ok)
                         break;
                     tc_fence_after();
                     const uint64_t ad = cdesc + (uint64_t)(c * (kBox >> 4));
-                    const uint64_t bd = (kind ? vdesc : kdesc) + (uint64_t)(st * (kStage >> 4));
+                    const uint64_t bd = (kind ? vdesc : kdesc) + (uint64_t)(st * (kBox >> 4));
 #pragma unroll
                     for (int i = 0; i < kChunk / 16; ++i)
-                        elect_ss(d, ad + i * 2, bd + i * step, idesc, (c | i) ? 1u : 0u);
-                    elect_commit(&B.b_empty[st]);
+                        elect_ss2(d, ad + i * 2, bd + i * step, idesc, (c | i) ? 1u : 0u);
+                    elect_commit2(&B.b_empty[st]);
                 }
                 if (ok)
-                    elect_commit(&B.d_full[buf]);
+                    elect_commit2(&B.d_full[buf]);
             }
             if (ok && last)
-                elect_commit(&B.a_empty);
+                elect_commit2(&B.a_empty);
             fresh = last;
         }
-        // every MMA issued here has completed before TMEM is freed
-        elect_commit(&B.done);
+        // every MMA has completed, and every commit has arrived, before either
+        // CTA frees its TMEM and exits
+        if (rank == 0)
+            elect_commit2(&B.done);
         ok = __all_sync(0xffffffffu, mbar_wait(&B.done, 0)) && ok;
     } else if (warp == 2) {
         // the shared rope keys of a tile's tokens, copied once, with its first unit
@@ -254,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; w.more(); w.next()) {
             if (w.group || w.pair || !vecs)
                 continue;
-            const ragged::Tile t = a.tiles[w.tile];
+            const ragged::Tile t = pair_tile(a, w, ntiles, rank);
             for (int i = lane; i < t.nq * vecs; i += 32) {
                 const int r = i / vecs, p = i % vecs;
                 const int page = page_or_none(a, t.seq, (t.tok0 + r) / kPage, false);
@@ -267,11 +358,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {
         // ----------------------------------------------- accumulators to memory
+        // A warp stores its 32 rows in boxes of 64 columns by TMA, through
+        // shared memory; where the sequence ends inside them, row by row (the
+        // rows behind are the next sequence's).
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const int r0 = (warp & 3) * 32 + lane;           // row of the tile
-        uint32_t nd = 0;
+        unsigned char *const out_box = outs + (warp & 3) * 2 * kOutBox;
+        uint32_t nd = 0, no = 0;
         for (; ok && w.more(); w.next()) {
-            const int q0 = a.tiles[w.tile].q0, nq = a.tiles[w.tile].nq;
+            const ragged::Tile t = pair_tile(a, w, ntiles, rank);
+            const int q0 = t.q0, nq = t.nq;
+            const bool whole = (warp & 3) * 32 + 32 <= nq;
             const int heads = min(2, a.heads_per_group - 2 * w.pair);
             const int h = w.group * a.heads_per_group + 2 * w.pair;
 #pragma unroll 1
@@ -282,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 tc_fence_after();
                 const int width = kind ? a.d_v : a.d_k;
-                const bool wide = kind ? a.wide_v : a.wide_k;
                 __nv_bfloat16 *const rows = (kind ? a.v : a.k) + ((long long)h * a.max_kv + q0 + r0) * width;
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 64) {
@@ -293,43 +389,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(&B.d_empty[buf]);
+                            mbar_arrive_cluster(mapa_shared(smem_u32(&B.d_empty[buf]), 0));
                     }
-                    __nv_bfloat16 *const out = rows + (long long)(c >> 7) * a.max_kv * width + (c & 64);
-                    if (r0 < nq && (c >> 7) < heads) {
+                    if ((c >> 7) >= heads || (c & 64) >= width)
+                        continue;
+                    uint4 v[8];
 #pragma unroll
-                        for (int i = 0; i < 64; i += 16) {
-                            uint32_t pk[8];
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t pk[4];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[i + 2 * j]),
-                                                                               __uint_as_float(r[i + 2 * j + 1]));
-                                pk[j] = *reinterpret_cast<const uint32_t *>(&v);
-                            }
-                            const int col = (c & 64) + i;
-                            if (wide && col + 16 <= width) {
-                                store32(out + i, pk);
-                            } else {
-                                if (col < width)
-                                    *reinterpret_cast<uint4 *>(out + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                                if (col + 8 < width)
-                                    *reinterpret_cast<uint4 *>(out + i + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * j]),
+                                                                           __uint_as_float(r[8 * i + 2 * j + 1]));
+                            pk[j] = *reinterpret_cast<const uint32_t *>(&x);
                         }
+                        v[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    if (whole) {
+                        unsigned char *const box = out_box + (no++ & 1) * kOutBox;
+                        if (lane == 0)
+                            tma_store_wait_read1();      // the box before last has been read
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = v[i];
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            tma_store_3d(kind ? &vout : &kout, c & 64, q0 + (warp & 3) * 32, h + (c >> 7), box);
+                    } else if (r0 < nq) {
+                        __nv_bfloat16 *const out = rows + (long long)(c >> 7) * a.max_kv * width + (c & 64);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if ((c & 64) + 8 * i < width)
+                                *reinterpret_cast<uint4 *>(out + 8 * i) = v[i];
                     }
                     __syncwarp();
                 }
             }
         }
+        if (lane == 0)
+            tma_store_wait_all();
+        __syncwarp();
     }
     if (!ok && lane == 0 && a.err)
         atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     if (warp == 0)
-        tmem_dealloc(tbase, 512);
+        tmem_dealloc2(tbase, 512);
 }
 
 }  // namespace
@@ -385,7 +495,7 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
         return KVATTN_OK;
     const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto swz = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap cm, km, vm;
+    CUtensorMap cm, km, vm, ko, vo;
     {
         const cuuint64_t dims[2] = {(cuuint64_t)pr.row, (cuuint64_t)pr.num_pages * kPage};
         const cuuint64_t strides[1] = {(cuuint64_t)pr.row * 2};
@@ -405,6 +515,14 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
         const cuuint64_t strides[2] = {(cuuint64_t)d_v * 2, (cuuint64_t)pr.dn * d_v * 2};
         const cuuint32_t box[3] = {64, kChunk, 1};
         if (encode_tiled(&vm, bf16, 3, const_cast<void *>(w_uv), dims, strides, box, swz) != CUDA_SUCCESS)
+            return KVATTN_ERR_UNSUPPORTED;
+    }
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t width = (cuuint64_t)(i ? d_v : d_k);
+        const cuuint64_t dims[3] = {width, (cuuint64_t)max_kv_tokens, (cuuint64_t)pr.H};
+        const cuuint64_t strides[2] = {width * 2, (cuuint64_t)max_kv_tokens * width * 2};
+        const cuuint32_t box[3] = {64, 32, 1};
+        if (encode_tiled(i ? &vo : &ko, bf16, 3, i ? v : k_nope, dims, strides, box, swz) != CUDA_SUCCESS)
             return KVATTN_ERR_UNSUPPORTED;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -433,8 +551,6 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.heads_per_group = pr.HPU;
     a.groups = pr.NU;
     a.pairs_per_group = pairs;
-    a.wide_k = d_k % 16 == 0 && is_aligned(k_nope, 32);
-    a.wide_v = d_v % 16 == 0 && is_aligned(v, 32);
     a.d_c = pr.dn;
     a.d_k = d_k;
     a.d_v = d_v;
@@ -443,12 +559,13 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.mpps = pr.mpps;
     a.num_pages = pr.num_pages;
     a.max_kv = max_kv_tokens;
-    const size_t smem = (size_t)(pr.dn / kChunk) * kBox + kStages * kStage + sizeof(Bars);
+    const int chunks = pr.dn / kChunk;
+    const size_t smem = (size_t)(chunks + stages_of(chunks)) * kBox + kOutBytes + sizeof(Bars);
     if (cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return KVATTN_ERR_CUDA;
-    const long long units = cap * pr.NU * pairs, sms = sm_count();
+    const long long units = (cap + 1) / 2 * pr.NU * pairs, most = sm_count() / 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units < sms ? units : sms));
+    cfg.gridDim = dim3((unsigned)(2 * (units < most ? units : most)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -457,6 +574,6 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expand_kernel, cm, km, vm, (const ExpandArgs)a) == cudaSuccess ? KVATTN_OK
+    return cudaLaunchKernelEx(&cfg, expand_kernel, cm, km, vm, ko, vo, (const ExpandArgs)a) == cudaSuccess ? KVATTN_OK
                                                                                                    : KVATTN_ERR_CUDA;
 }
