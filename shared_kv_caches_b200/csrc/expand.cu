@@ -150,32 +150,47 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int 
 __device__ __forceinline__ void tma_store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// The units of this cluster, in order; every role walks them on its own.
+// The units of this cluster, in order; every role walks them on its own.  While
+// there are tile pairs for all clusters, each takes one whole, so that they
+// stream the same weights at about the same time (out of L2, where the outputs
+// would push weights out between uses far apart); what is left is cut into
+// equal runs of units.
 struct Walk {
-    int unit, end;                               // of (tile pair, group, head pair), heads fastest
+    int unit, whole, end;                        // units done, of whole tile pairs, and in all
+    int first;                                   // where the run of what is left starts
     int pairs, groups;
     int tiles, group, pair;
-    __device__ __forceinline__ Walk(const ExpandArgs &a, int ntiles) : pairs(a.pairs_per_group), groups(a.groups)
+    __device__ __forceinline__ Walk(const ExpandArgs &a, int ntiles)
+        : unit(0), pairs(a.pairs_per_group), groups(a.groups), tiles(blockIdx.x / 2), group(0), pair(0)
     {
-        const long long all = (long long)((ntiles + 1) / 2) * groups * pairs;
-        const unsigned c = blockIdx.x / 2, n = gridDim.x / 2;
-        unit = (int)(all * c / n);
-        end = (int)(all * (c + 1) / n);
-        pair = unit % pairs;
-        group = unit / pairs % groups;
-        tiles = unit / pairs / groups;
+        const int c = blockIdx.x / 2, n = gridDim.x / 2, all = (ntiles + 1) / 2, each = groups * pairs;
+        const int rounds = all / n;
+        const long long left = (long long)(all - rounds * n) * each;
+        const int from = (int)(left * c / n), to = (int)(left * (c + 1) / n);
+        whole = rounds * each;
+        end = whole + to - from;
+        first = rounds * n * each + from;
+        if (rounds == 0)
+            start_rest();
+    }
+    __device__ __forceinline__ void start_rest()
+    {
+        pair = first % pairs;
+        group = first / pairs % groups;
+        tiles = first / pairs / groups;
     }
     __device__ __forceinline__ bool more() const { return unit < end; }
     // whether the unit after this one has other latents (or there is none)
     __device__ __forceinline__ bool last_of_latents() const { return pair + 1 == pairs || unit + 1 == end; }
     __device__ __forceinline__ void next()
     {
-        ++unit;
-        if (++pair == pairs) {
+        if (++unit == whole) {
+            start_rest();
+        } else if (++pair == pairs) {
             pair = 0;
             if (++group == groups) {
                 group = 0;
-                ++tiles;
+                tiles += unit < whole ? (int)gridDim.x / 2 : 1;
             }
         }
     }
