@@ -19,7 +19,7 @@
 // latents in place and a head's weights read once for two tiles, an SM reads
 // 32 bytes a cycle from L2 while its MMAs run; one CTA on its own needs 64, and
 // the 96 KB that it can have in flight are then no more than the latency
-// times that (818 against ... us).  Every cluster takes the same number of
+// times that (ragged MLA prompts, 22 thousand tokens: 818 us; so, 681).  Every cluster takes the same number of
 // (tile pair, group, head pair) units, in order, and loads latents only where
 // the tiles or the group change.
 #include <math.h>
@@ -101,11 +101,12 @@ __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, 
                  : "memory");
 }
 
-__device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+__device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar,
+                                             uint64_t policy)
 {
-    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-                 "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+                 "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
                  : "memory");
 }
 
@@ -135,13 +136,30 @@ __device__ __forceinline__ int page_or_none(const ExpandArgs &a, int seq, int pi
     return (int)page;
 }
 
+// L2 keeps the weights, which every cluster reads again for every tile pair,
+// rather than the outputs, which are more than it holds (GLA 16K 360 -> 332 us,
+// ragged MLA prompts 596 -> 590).
+__device__ __forceinline__ uint64_t keep_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ uint64_t pass_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // TMA store of a box from shared memory, and the groups that such stores are
 // waited for in.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, const void *src)
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, const void *src, uint64_t policy)
 {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -254,6 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA
         if (lane == 0) {
+            const uint64_t policy = keep_policy();
             uint32_t nb = 0, na = 0;             // weight chunks, latent tiles loaded
             bool fresh = true;
             for (; ok && w.more(); w.next()) {
@@ -290,10 +309,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (rank == 0)
                             mbar_arrive_expect_tx(&B.b_full[st], 2 * kBox);
                         if (kind == 0) {
-                            pair_load_3d(dst, &kmap, c * kChunk, 0, h, bar);
+                            pair_load_3d(dst, &kmap, c * kChunk, 0, h, bar, policy);
                         } else {
-                            pair_load_3d(dst, &vmap, 0, c * kChunk, h, bar);
-                            pair_load_3d(dst + kBox / 2, &vmap, 64, c * kChunk, h, bar);
+                            pair_load_3d(dst, &vmap, 0, c * kChunk, h, bar, policy);
+                            pair_load_3d(dst + kBox / 2, &vmap, 64, c * kChunk, h, bar, policy);
                         }
                     }
             }
@@ -379,6 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const int r0 = (warp & 3) * 32 + lane;           // row of the tile
         unsigned char *const out_box = outs + (warp & 3) * 2 * kOutBox;
+        const uint64_t policy = pass_policy();
         uint32_t nd = 0, no = 0;
         for (; ok && w.more(); w.next()) {
             const ragged::Tile t = pair_tile(a, w, ntiles, rank);
@@ -431,7 +451,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0)
-                            tma_store_3d(kind ? &vout : &kout, c & 64, q0 + (warp & 3) * 32, h + (c >> 7), box);
+                            tma_store_3d(kind ? &vout : &kout, c & 64, q0 + (warp & 3) * 32, h + (c >> 7), box,
+                                         policy);
                     } else if (r0 < nq) {
                         __nv_bfloat16 *const out = rows + (long long)(c >> 7) * a.max_kv * width + (c & 64);
 #pragma unroll
