@@ -11,11 +11,11 @@
 //   pos(t)  = c_b + t - q_start_b
 //   page(i) = i-th entry from the top of the free list for the request's new
 //             pages, the table's entry for the page it already holds
-// The whole call is one launch of one thread-block cluster: every CTA repeats
-// the sums (a few thousand integers) and takes a share of the tokens and
-// pages, and the lengths and the free count are written after a cluster
-// barrier, when every CTA has read them, so they may be updated in place (a
-// captured decode step advances by itself on each replay).
+// The whole call is one launch: every CTA repeats the sums (a few thousand
+// integers) and takes a share of the tokens and pages.  Where the lengths and
+// the free count are updated in place (a captured decode step advances by
+// itself on each replay), the CTAs are one thread-block cluster, and the new
+// values are written after its barrier, when every CTA has read the old.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -33,6 +33,7 @@ constexpr int kTokensPerCta = 4096;
 
 struct TableArgs {
     int batch, mpps, num_pages, max_tokens;
+    int vectors;                                    // pos and slots start on 16 bytes
     const int32_t *cached, *fresh, *free_pages, *free_count;
     int32_t *table, *seq_lens, *free_left, *q_start, *kv_start, *pos, *slots, *err;
 };
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
         atomicMax(&sh_taken, taken);
     if (rank == 0 && bits && a.err)
         atomicOr(a.err, bits);
-    // every CTA has read the lengths and the free count
+    // every CTA of the cluster (or this one alone) has read the lengths and the free count
     cluster_sync_all();
     taken = sh_taken;
 
@@ -149,27 +150,47 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
             bits = KVATTN_DEVERR_PAGE_OUT_OF_RANGE;
         a.table[(long long)b * a.mpps + pages_of(cch[b]) + i - pgs[b]] = page;
     }
-#pragma unroll 4
-    for (int t = rank * kTableThreads + tid; t < total; t += ctas * kTableThreads) {
-        const int b = ragged::find(tok, a.batch, t);
-        const int c = cch[b];
-        const long long p = (long long)(c >= 0 ? c : -1 - c) + t - tok[b];
-        int slot = -1;
-        if (c >= 0) {
+    // four tokens at a time: one search, and one page looked up, for most
+    for (int t0 = 4 * (rank * kTableThreads + tid); t0 < a.max_tokens; t0 += 4 * ctas * kTableThreads) {
+        int pos[4], slot[4];
+        int b = t0 < total ? ragged::find(tok, a.batch, t0) : 0;
+        int c = 0, at = -1, page = -1;                  // the request's cached tokens; the page looked up last
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int t = t0 + k;
+            pos[k] = 0;
+            slot[k] = -1;
+            if (t >= total)
+                continue;
+            if (k == 0 || t >= tok[b + 1]) {
+                while (t >= tok[b + 1])
+                    ++b;
+                c = cch[b];
+                at = -1;
+            }
+            const long long p = (long long)(c >= 0 ? c : -1 - c) + t - tok[b];
+            pos[k] = (int)min(p, (long long)INT32_MAX);
+            if (c < 0)
+                continue;
             const int pi = (int)(p / kPage), held = pages_of(c);
-            const int page = pi < held ? a.table[(long long)b * a.mpps + pi]
-                                       : a.free_pages[nfree - 1 - (pgs[b] + pi - held)];
+            if (pi != at) {
+                at = pi;
+                page = pi < held ? a.table[(long long)b * a.mpps + pi] : a.free_pages[nfree - 1 - (pgs[b] + pi - held)];
+            }
             if (page < 0 || page >= a.num_pages)
                 bits = KVATTN_DEVERR_PAGE_OUT_OF_RANGE;
             else
-                slot = page * kPage + (int)(p % kPage);
+                slot[k] = page * kPage + (int)(p % kPage);
         }
-        a.pos[t] = (int)min(p, (long long)INT32_MAX);
-        a.slots[t] = slot;
-    }
-    for (int t = total + rank * kTableThreads + tid; t < a.max_tokens; t += ctas * kTableThreads) {
-        a.pos[t] = 0;
-        a.slots[t] = -1;
+        if (a.vectors && t0 + 4 <= a.max_tokens) {
+            *reinterpret_cast<int4 *>(a.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+            for (int k = 0; k < 4 && t0 + k < a.max_tokens; ++k) {
+                a.pos[t0 + k] = pos[k];
+                a.slots[t0 + k] = slot[k];
+            }
+        }
     }
     if (bits && a.err)
         atomicOr(a.err, bits);
@@ -193,9 +214,16 @@ struct SlotAppendArgs {
     float k_scale, v_scale;       // fp8: what a stored value is multiplied by when it is read
 };
 
+// Turns (of pi) that pair i of a width-wide slice makes per position.
 __device__ __forceinline__ double rope_rate(int i, int width, double log2_base)
 {
-    return exp2(-2.0 * (double)i / (double)width * log2_base);
+    return exp2(-2.0 * (double)i / (double)width * log2_base) * 0.31830988618379067;
+}
+
+// x / scale in fp32; exactly the product with 1 / scale where that is a power of two.
+__device__ __forceinline__ float unscaled(float x, float scale, float inverse, bool exact)
+{
+    return exact ? x * inverse : x / scale;
 }
 
 // Two values as e4m3 bytes, nearest even, saturated at +-448.
@@ -207,22 +235,34 @@ __device__ __forceinline__ uint16_t e4m3_pair(float x, float y)
 // Eight bf16 values divided by scale, as e4m3 bytes.
 __device__ __forceinline__ uint2 e4m3_oct(uint4 v, float scale)
 {
+    // a product is a tenth of a division's instructions (fp8 append of 9001
+    // tokens: 31 -> 20 us)
+    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0 && scale > 1e-30f && scale < 1e30f;
+    const float inverse = 1.f / scale;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        r[i] = e4m3_pair(__uint_as_float(w[i] << 16) / scale, __uint_as_float(w[i] & 0xffff0000u) / scale);
+        r[i] = e4m3_pair(unscaled(__uint_as_float(w[i] << 16), scale, inverse, exact),
+                         unscaled(__uint_as_float(w[i] & 0xffff0000u), scale, inverse, exact));
     return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
+
+// Four 16-byte vectors a lane at a time: 2 KB of a row on their way per warp.
+constexpr int kAppendVecs = 4;
+// Heads whose pairs a lane loads before it forms their angle.
+constexpr int kAppendHeads = 8;
 
 // One warp per token: 16-byte copies of what is stored as it is; a turned
 // pair belongs to one lane, which forms its angle once for the token and turns
 // the pair of every slice (every K head) with it.  The angle and the turn are
-// in double precision with one rounding to the stored type, as kvattn_rope's;
-// a lane's first two rates (all it has for slices up to 128 wide) stay in
-// registers over its tokens.
+// in double precision with one rounding to the stored type, as kvattn_rope's
+// (in turns of pi: the whole turns of a far position come off exactly); a lane's first two rates (all it has for slices up to 128 wide) stay in
+// registers over its tokens.  Bound by memory latency: a row's loads do not
+// wait for its slot or for the angles, which are formed while they are under
+// way.
 template <bool FP8>
-__global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const SlotAppendArgs a)
+__global__ void __launch_bounds__(kAppendThreads, 4) append_slots_kernel(const SlotAppendArgs a)
 {
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (kAppendThreads / 32);
@@ -230,56 +270,78 @@ __global__ void __launch_bounds__(kAppendThreads) append_slots_kernel(const Slot
     double rate0 = 0.0, rate1 = 0.0;
     if (a.rot_count > 0) {
         rate0 = rope_rate(lane, a.rot_width, a.log2_base);
-        rate1 = rope_rate(lane + 32, a.rot_width, a.log2_base);
+        if (half > 32)
+            rate1 = rope_rate(lane + 32, a.rot_width, a.log2_base);
     }
     for (int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < a.tokens; t += warps) {
         const int slot = a.slots[t];
-        if (slot < 0 || slot >= a.num_slots) {
-            if (slot != -1 && lane == 0 && a.err)
-                atomicOr(a.err, KVATTN_DEVERR_PAGE_OUT_OF_RANGE);
-            continue;
-        }
+        const int pos = a.rot_count > 0 ? a.pos[t] : 0;
+        const bool valid = slot >= 0 && slot < a.num_slots;
         const long long page = slot / kPage;
         const int off = slot % kPage;
         for (int pl = 0; pl < a.planes; ++pl) {
             const __nv_bfloat16 *src = a.src + ((long long)t * a.planes + pl) * a.row;
             const long long at = ((page * a.planes + pl) * kPage + off) * (long long)a.row;
             const bool turn = a.rot_count > 0 && pl == 0;
-            const int copy = turn ? a.copy : a.row;
+            const int copy = turn ? a.copy : a.row, vecs = copy / 8;
             const float scale = pl == 0 ? a.k_scale : a.v_scale;
-#pragma unroll 4
-            for (int i = lane; i < copy / 8; i += 32) {
-                const uint4 v = reinterpret_cast<const uint4 *>(src)[i];
-                if constexpr (FP8)
-                    reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache) + at)[i] = e4m3_oct(v, scale);
-                else
-                    reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + at)[i] = v;
+            for (int i0 = lane; i0 < vecs; i0 += 32 * kAppendVecs) {
+                uint4 v[kAppendVecs];
+#pragma unroll
+                for (int x = 0; x < kAppendVecs; ++x)
+                    if (i0 + 32 * x < vecs)
+                        v[x] = __ldcs(reinterpret_cast<const uint4 *>(src) + i0 + 32 * x);
+                if (!valid)
+                    break;
+#pragma unroll
+                for (int x = 0; x < kAppendVecs; ++x) {
+                    const int i = i0 + 32 * x;
+                    if (i >= vecs)
+                        break;
+                    if constexpr (FP8)
+                        reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache) + at)[i] = e4m3_oct(v[x], scale);
+                    else
+                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + at)[i] = v[x];
+                }
             }
-            if (!turn)
+            if (!turn || !valid)
                 continue;
-            const double p = (double)a.pos[t];
+            const double unscale = 1.0 / (double)scale;
             for (int i = lane; i < half; i += 32) {
                 const double rate = i == lane ? rate0 : i == lane + 32 ? rate1 : rope_rate(i, a.rot_width, a.log2_base);
-                double s, c;
-                sincos(p * rate, &s, &c);
-#pragma unroll 4
-                for (int n = 0; n < a.rot_count; ++n) {
-                    const int e = copy + n * a.rot_width + 2 * i;
-                    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(src + e);
-                    const double x = (double)__bfloat162float(v.x), y = (double)__bfloat162float(v.y);
-                    const double rx = x * c - y * s, ry = x * s + y * c;
-                    if constexpr (FP8) {
-                        *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.cache) + at + e) =
-                            e4m3_pair((float)(rx / (double)scale), (float)(ry / (double)scale));
-                    } else {
-                        __nv_bfloat162 r;
-                        r.x = __double2bfloat16(rx);
-                        r.y = __double2bfloat16(ry);
-                        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.cache) + at + e) = r;
+                double s = 0.0, c = 1.0;
+                for (int n0 = 0; n0 < a.rot_count; n0 += kAppendHeads) {
+                    __nv_bfloat162 v[kAppendHeads];
+#pragma unroll
+                    for (int n = 0; n < kAppendHeads; ++n)
+                        if (n0 + n < a.rot_count)
+                            v[n] = *reinterpret_cast<const __nv_bfloat162 *>(src + copy + (n0 + n) * a.rot_width + 2 * i);
+                    if (n0 == 0)
+                        sincospi((double)pos * rate, &s, &c);
+#pragma unroll
+                    for (int n = 0; n < kAppendHeads; ++n) {
+                        if (n0 + n >= a.rot_count)
+                            break;
+                        const int e = copy + (n0 + n) * a.rot_width + 2 * i;
+                        const double x = (double)__bfloat162float(v[n].x), y = (double)__bfloat162float(v[n].y);
+                        const double rx = x * c - y * s, ry = x * s + y * c;
+                        if constexpr (FP8) {
+                            // one rounding to e4m3 but for the one to fp32 in
+                            // front of it, 20 bits finer
+                            *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.cache) + at + e) =
+                                e4m3_pair((float)(rx * unscale), (float)(ry * unscale));
+                        } else {
+                            __nv_bfloat162 r;
+                            r.x = __double2bfloat16(rx);
+                            r.y = __double2bfloat16(ry);
+                            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.cache) + at + e) = r;
+                        }
                     }
                 }
             }
         }
+        if (!valid && slot != -1 && lane == 0 && a.err)
+            atomicOr(a.err, KVATTN_DEVERR_PAGE_OUT_OF_RANGE);
     }
 }
 
@@ -310,10 +372,16 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
                           static_cast<const void *>(slots), static_cast<const void *>(device_error)})
         if (!is_aligned(p, 4))
             return KVATTN_ERR_MISALIGNED;
-    TableArgs a{batch, max_pages_per_seq, num_pages, max_tokens, cached_lens, new_lens, free_pages, free_count,
+    TableArgs a{batch, max_pages_per_seq, num_pages, max_tokens,
+                is_aligned(pos, 16) && is_aligned(slots, 16), cached_lens, new_lens, free_pages, free_count,
                 block_table, seq_lens, free_left, q_start, kv_start, pos, slots, device_error};
     int ctas = (max_tokens + kTokensPerCta - 1) / kTokensPerCta;
-    ctas = ctas < 1 ? 1 : ctas > kTableMaxCtas ? kTableMaxCtas : ctas;
+    // in place, what one CTA writes others read: a cluster of up to eight.
+    // Otherwise as many as there are tokens for (150 thousand: 13 us with
+    // eight, 6 with 37)
+    const bool in_place = seq_lens == cached_lens || free_left == free_count;
+    const int most = in_place ? kTableMaxCtas : sm_count();
+    ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
     const size_t smem = (3 * (size_t)batch + 2) * sizeof(int32_t);
     if (smem > 48 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem) != cudaSuccess)
@@ -329,7 +397,7 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = in_place && ctas > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, build_tables_kernel, (const TableArgs)a) == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
 }
 
@@ -378,7 +446,7 @@ extern "C" int kvattn_append_slots(int32_t variant, const kvattn_params *p, cons
     }
     const int per = kAppendThreads / 32;
     const long long want = ((long long)num_tokens + per - 1) / per;
-    const long long most = 8LL * sm_count();      // eight resident blocks an SM: every SM full, rates kept over tokens
+    const long long most = 4LL * sm_count();      // the blocks that are resident: rates are formed once a warp
     const int grid = (int)(want < most ? want : most);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (fp8)

@@ -383,21 +383,20 @@ def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_ta
     n = int(max_tokens)
     if cached_lens.shape[0] != B or new_lens.shape[0] != B or free_count.shape[0] != 1 or n < 0:
         raise ValueError("cached_lens, new_lens and block_table have one row a request, free_count one value")
-    # the outputs share one allocation
-    sizes = [B + 1, B + 1, n, n] if inplace else [B + 1, B + 1, n, n, B, 1]
+    # the outputs share one allocation, pos and slots in front (on 16 bytes)
+    sizes = [n, n, B + 1, B + 1] if inplace else [n, n, B + 1, B + 1, B, 1]
     r = torch.empty(sum(sizes), dtype=i32, device=dev)
-    at = r.data_ptr()
-    ptr = [at, at + 4 * (B + 1), at + 8 * (B + 1), at + 8 * (B + 1) + 4 * n]
+    pos = r.data_ptr()
+    slots, q_start, kv_start, end = pos + 4 * n, pos + 8 * n, pos + 8 * n + 4 * B + 4, pos + 8 * n + 8 * B + 8
     if inplace:
         lens, left = cached_lens.data_ptr(), free_count.data_ptr()
     else:
-        lens = ptr[3] + 4 * n
-        left = lens + 4 * B
+        lens, left = end, end + 4 * B
     _enqueue("kvattn_build_tables", dev, load().kvattn_build_tables, B, mpps, free_pages.shape[0], n,
              cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-             block_table.data_ptr(), lens, left, *ptr, _error_word(device_error, dev))
+             block_table.data_ptr(), lens, left, q_start, kv_start, pos, slots, _error_word(device_error, dev))
     v = r.split(sizes)
-    return dict(block_table=block_table, q_start=v[0], kv_start=v[1], pos=v[2], slots=v[3],
+    return dict(block_table=block_table, pos=v[0], slots=v[1], q_start=v[2], kv_start=v[3],
                 seq_lens=cached_lens if inplace else v[4], free_left=free_count if inplace else v[5])
 
 
