@@ -86,6 +86,7 @@ struct PrefillArgs {
     int32_t *err;                                 // may be null
     int heads, heads_per_kv;
     int d_v, out_fp32, causal;
+    int wide;                                     // output rows start on 32 bytes
     long long out_token_stride, out_head_stride;
     float scale_log2;
 };
@@ -105,13 +106,21 @@ struct Layout {
     static_assert(kBytes <= kSmemMax, "shared memory");
 };
 
-// The item numbers that the TMA thread hands out, two at a time.
+// A work item: a tile of the list, a head, and the key tiles of its two query tiles.
+struct Item {
+    int32_t q0, nq, k0, nk, lim0;                 // as in ragged::Tile
+    int32_t head;                                 // -1: no more items
+    int32_t n0, n1;
+};
+
+// The items that the TMA thread hands out stand here until all have read them.
+constexpr int kItems = 4;
 constexpr int kItemReaders = 10;                  // the MMA warps and the softmax warps
 
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t item_full[2], item_empty[2];
-    int32_t item[2];
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item item[kItems];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], s_free[2];                // scores formed; scores in registers
     uint64_t p_full[2];                           // probabilities stored
@@ -201,13 +210,6 @@ __device__ __forceinline__ void exp2_fma(float &e0, float &e1, float x0, float x
           __uint_as_float((__float_as_uint(t1) << 23) + 0x3F800000u));
 }
 
-// Work item i: its tile, its head, and the key tiles of its two query tiles.
-struct Item {
-    ragged::Tile t;
-    int head;
-    int n0, n1;
-};
-
 __device__ __forceinline__ int key_end(const PrefillArgs &a, const ragged::Tile &t, int rows_before, int rows)
 {
     // keys that the last of `rows` rows from rows_before on attends
@@ -216,16 +218,38 @@ __device__ __forceinline__ int key_end(const PrefillArgs &a, const ragged::Tile 
     return a.causal ? min(t.nk, max(t.lim0 + rows_before + rows - 1, 0)) : t.nk;
 }
 
+// N words of a row: with `wide` (rows that start on 32 bytes) a whole sector at a time.
+template <int N>
+__device__ __forceinline__ void store_row(void *p, const uint32_t *r, bool wide)
+{
+    if constexpr (N == 8) {
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+                         "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                         : "memory");
+            return;
+        }
+        static_cast<uint4 *>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+    static_cast<uint4 *>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Item i of the list: groups of kHeadGroup heads, then tiles, then heads.
 __device__ __forceinline__ Item get_item(const PrefillArgs &a, int ntiles, int i)
 {
-    Item it;
     const int per_group = ntiles * kHeadGroup;
     const int g = i / per_group, r = i - g * per_group;
     const int hc = min(kHeadGroup, a.heads - g * kHeadGroup);
-    it.t = a.tiles[r / hc];
+    const ragged::Tile t = a.tiles[r / hc];
+    Item it;
+    it.q0 = t.q0;
+    it.nq = t.nq;
+    it.k0 = t.k0;
+    it.nk = t.nk;
+    it.lim0 = t.lim0;
     it.head = g * kHeadGroup + r % hc;
-    it.n0 = (key_end(a, it.t, 0, min(it.t.nq, kTile)) + kKeys - 1) / kKeys;
-    it.n1 = (key_end(a, it.t, kTile, it.t.nq - kTile) + kKeys - 1) / kKeys;
+    it.n0 = (key_end(a, t, 0, min(t.nq, kTile)) + kKeys - 1) / kKeys;
+    it.n1 = (key_end(a, t, kTile, t.nq - kTile) + kKeys - 1) / kKeys;
     return it;
 }
 
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B.p_free[i], 1);
             mbar_init(&B.o_full[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kItems; ++i) {
             mbar_init(&B.item_full[i], 1);
             mbar_init(&B.item_empty[i], kItemReaders);
         }
@@ -278,25 +302,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tbase + 256;                     // + kKeys for the second query tile
     const uint32_t tP = tS + 2 * kKeys;
     pdl_wait_primary();                                  // the tile list
-    const int ntiles = a.header[0];
-    const int items = ntiles * a.heads;
     bool ok = true;
-    // The next item, for a whole warp: -1 at the end or where a wait ran out.
+    // The next item, for a whole warp: null at the end or where a wait ran out.
+    // It stays until the warp has called done_item.
     uint32_t taken = 0;
-    auto next_item = [&]() -> int {
-        const int slot = taken & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&B.item_full[slot], (taken >> 1) & 1))) {
+    auto next_item = [&]() -> const Item * {
+        const uint32_t slot = taken % kItems;
+        if (!__all_sync(0xffffffffu, mbar_wait(&B.item_full[slot], (taken / kItems) & 1))) {
             ok = false;
-            return -1;
+            return nullptr;
         }
-        const int i = B.item[slot];
+        return B.item[slot].head < 0 ? nullptr : &B.item[slot];
+    };
+    auto done_item = [&]() {
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(&B.item_empty[slot]);
+            mbar_arrive(&B.item_empty[taken % kItems]);
         ++taken;
-        return i;
     };
-
     // Every MMA that this warp issued has completed (before TMEM is freed).
     auto finish = [&]() {
         elect_commit(&B.mma_done[warp - 1]);
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++qn[i];
                 mbar_arrive_expect_tx(&B.q_full[i], NKB * kQBox);
-                const int row = it.t.q0 + i * kTile;
+                const int row = it.q0 + i * kTile;
 #pragma unroll
                 for (int b = 0; b < NKB; ++b) {
                     unsigned char *dst = smem + (i * NKB + b) * kQBox;
@@ -330,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto load_k = [&](const Item &it, int j) {
-                const int row = it.t.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = kn & 1;
+                const int row = it.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = kn & 1;
                 if (kn >= 2 && !mbar_wait(&B.k_empty[st], ((kn >> 1) - 1) & 1)) {
                     ok = false;
                     return;
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto load_v = [&](const Item &it, int j) {
-                const int row = it.t.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = vn & 1;
+                const int row = it.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = vn & 1;
                 if (vn >= 2 && !mbar_wait(&B.v_empty[st], ((vn >> 1) - 1) & 1)) {
                     ok = false;
                     return;
@@ -361,19 +384,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // items are handed out as CTAs get to them: the first by the block's
             // number, then by a count that the plan kernel sets to 0
+            const int ntiles = a.header[0], items = ntiles * a.heads;
             int i = blockIdx.x;
-            for (uint32_t given = 0;; ++given) {
-                const int slot = given & 1;
-                if (!ok || (given >= 2 && !mbar_wait(&B.item_empty[slot], ((given >> 1) - 1) & 1))) {
+            for (uint32_t given = 0; ok; ++given) {
+                const uint32_t slot = given % kItems;
+                Item it{};
+                it.head = -1;
+                const bool any = i < items;
+                if (any) {
+                    it = get_item(a, ntiles, i);
+                    i = (int)gridDim.x + atomicAdd(&a.header[1], 1);
+                }
+                if (given >= kItems && !mbar_wait(&B.item_empty[slot], (given / kItems - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                B.item[slot] = i < items ? i : -1;
+                B.item[slot] = it;
                 mbar_arrive(&B.item_full[slot]);
-                if (i >= items)
+                if (!any)
                     break;
-                const Item it = get_item(a, ntiles, i);
-                i = (int)gridDim.x + atomicAdd(&a.header[1], 1);
                 const int n = max(it.n0, it.n1);
                 if (n == 0)
                     continue;
@@ -412,13 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // phase bit i of query tile i: queries, scores taken to registers (the
         // first tile's columns are free from the start)
         uint32_t qpar = 0, fpar = 3;
-        for (int w; ok && (w = next_item()) >= 0;) {
-            int n0, n1;
-            {
-                const Item it = get_item(a, ntiles, w);
-                n0 = __shfl_sync(0xffffffffu, it.n0, 0);
-                n1 = __shfl_sync(0xffffffffu, it.n1, 0);
-            }
+        for (const Item *it; ok && (it = next_item());) {
+            const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
+            done_item();
             const int n = max(n0, n1);
 #pragma unroll 1
             for (int x = 0; x < 2 * n; ++x) {
@@ -460,14 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kValuesAt, kBox, 1024, 2);  // N-major value boxes
         uint32_t t = 0;                                  // value tiles of the items before
         uint32_t ppar = 0;                               // phase bit i: probabilities of query tile i
-        for (int w; ok && (w = next_item()) >= 0;) {
-            int n0, n1, nk;
-            {
-                const Item it = get_item(a, ntiles, w);
-                n0 = __shfl_sync(0xffffffffu, it.n0, 0);
-                n1 = __shfl_sync(0xffffffffu, it.n1, 0);
-                nk = __shfl_sync(0xffffffffu, it.t.nk, 0);
-            }
+        for (const Item *it; ok && (it = next_item());) {
+            const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
+            const int nk = __shfl_sync(0xffffffffu, it->nk, 0);
+            done_item();
             const int n = max(n0, n1);
             // the first to store probabilities waits for all items before
             if (n > 0)
@@ -534,13 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t p_addr = tP + lane_addr;
         const float c = a.scale_log2;
         uint32_t sn = 0, on = 0;                         // score tiles and outputs taken
-        for (int w; ok && (w = next_item()) >= 0;) {
-            int n, lim;
-            {
-                const Item it = get_item(a, ntiles, w);
-                n = i ? it.n1 : it.n0;
-                lim = a.causal ? min(it.t.nk, it.t.lim0 + row) : it.t.nk;
-            }
+        for (const Item *it; ok && (it = next_item());) {
+            const int n = i ? it->n1 : it->n0;
+            const int lim = a.causal ? min(it->nk, it->lim0 + row) : it->nk;
             const int lim_first = __shfl_sync(0xffffffffu, lim, 0);     // limits grow with the row
             float m_ref = -INFINITY, l = 0.f;
             const float none = c >= 0.f ? -INFINITY : INFINITY;
@@ -646,44 +663,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++on;
                 tc_fence_after();
             }
-            const Item it = get_item(a, ntiles, w);      // again: kept, it would cost the loop its registers
-            const bool valid = row < it.t.nq;
+            const bool valid = row < it->nq;
+            const int head = it->head;
+            const long long grow = (long long)it->q0 + row;
+            done_item();
             const bool any = n > 0 && l != 0.f;          // a row without keys has l = 0 (NaN passes)
             const float inv = any ? 1.f / l : 0.f;
-            const long long grow = (long long)it.t.q0 + row;
-            const long long at = grow * a.out_token_stride + it.head * a.out_head_stride;
+            const long long at = grow * a.out_token_stride + head * a.out_head_stride;
 #pragma unroll 1
-            for (int x = 0; x < kDv; x += 32) {
-                uint32_t r[32];
-                if (n > 0)
-                    tmem_ld32(o_addr + x, r);
+            for (int x = 0; x < kDv; x += 64) {
+                float f[64];
+                if (n > 0) {
+                    tmem_ld32_start(o_addr + x, f);
+                    tmem_ld32_start(o_addr + x + 32, f + 32);
+                    tmem_ld_wait(f);
+                    tmem_ld_wait(f + 32);
+                }
 #pragma unroll
-                for (int y = 0; y < 32; y += 8) {
-                    float f[8];
+                for (int y = 0; y < 64; ++y)
+                    f[y] = any ? f[y] * inv : 0.f;
+                if (valid && x < a.d_v) {
+                    if (a.out_fp32) {
+                        float *const dst = static_cast<float *>(a.out) + at + x;
 #pragma unroll
-                    for (int z = 0; z < 8; ++z)
-                        f[z] = any ? __uint_as_float(r[y + z]) * inv : 0.f;
-                    if (!valid || x + y >= a.d_v) {
-                        // nothing to store
-                    } else if (a.out_fp32) {
-                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + x + y);
-                        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-                        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+                        for (int y = 0; y < 64; y += 8)
+                            if (x + y < a.d_v)
+                                store_row<8>(dst + y, reinterpret_cast<const uint32_t *>(f + y), a.wide);
                     } else {
-                        uint32_t p[4];
+                        __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.out) + at + x;
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(f[2 * z], f[2 * z + 1]);
-                            p[z] = *reinterpret_cast<const uint32_t *>(&v2);
+                        for (int y = 0; y < 64; y += 16) {
+                            uint32_t p[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) {
+                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(f[y + 2 * z], f[y + 2 * z + 1]);
+                                p[z] = *reinterpret_cast<const uint32_t *>(&v2);
+                            }
+                            if (x + y + 8 < a.d_v)
+                                store_row<8>(dst + y, p, a.wide);
+                            else if (x + y < a.d_v)
+                                store_row<4>(dst + y, p, false);
                         }
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at + x + y) =
-                            make_uint4(p[0], p[1], p[2], p[3]);
                     }
                 }
                 __syncwarp();
             }
             if (valid && a.lse)
-                a.lse[grow * a.heads + it.head] = any ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+                a.lse[grow * a.heads + head] = any ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
             // the next item's first P.V overwrites the output: it follows this
             // warp's next arrival, which follows these loads
             tc_fence_before();
@@ -871,6 +897,7 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     a.d_v = p->d_v;
     a.out_fp32 = p->out_dtype == KVATTN_OUT_FP32;
     a.causal = p->causal;
+    a.wide = is_aligned(out, 32) && so[0] % (a.out_fp32 ? 8 : 16) == 0 && so[1] % (a.out_fp32 ? 8 : 16) == 0;
     a.out_token_stride = so[0];
     a.out_head_stride = so[1];
     // masked scores are infinite, so a scale of 0 (every key weighs the same)
