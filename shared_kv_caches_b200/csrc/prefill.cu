@@ -384,28 +384,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // items are handed out as CTAs get to them: the first by the block's
             // number, then by a count that the plan kernel sets to 0
+            // (an item is looked up while the one before is loaded)
             const int ntiles = a.header[0], items = ntiles * a.heads;
-            int i = blockIdx.x;
-            for (uint32_t given = 0; ok; ++given) {
-                const uint32_t slot = given % kItems;
+            auto look_up = [&](int i) -> Item {
                 Item it{};
                 it.head = -1;
-                const bool any = i < items;
-                if (any) {
-                    it = get_item(a, ntiles, i);
-                    i = (int)gridDim.x + atomicAdd(&a.header[1], 1);
-                }
+                return i < items ? get_item(a, ntiles, i) : it;
+            };
+            Item next = look_up(blockIdx.x);
+            for (uint32_t given = 0; ok; ++given) {
+                const uint32_t slot = given % kItems;
+                const Item it = next;
                 if (given >= kItems && !mbar_wait(&B.item_empty[slot], (given / kItems - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 B.item[slot] = it;
                 mbar_arrive(&B.item_full[slot]);
-                if (!any)
+                if (it.head < 0)
                     break;
+                const int after = (int)gridDim.x + atomicAdd(&a.header[1], 1);
                 const int n = max(it.n0, it.n1);
-                if (n == 0)
+                if (n == 0) {
+                    next = look_up(after);
                     continue;
+                }
                 if (it.n0 > 0)
                     load_q(it, 0);
                 if (ok)
@@ -417,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load_k(it, j + 1);
                     if (ok)
                         load_v(it, j);
+                    if (j == 0)
+                        next = look_up(after);
                 }
             }
             // every copy started here has landed before the CTA can exit
