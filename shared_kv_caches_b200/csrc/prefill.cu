@@ -7,14 +7,19 @@
 //
 // One CTA works off 256 query rows of one head (two MMA tiles of 128) against
 // key tiles of 96 tokens in one pass with a running maximum and sum.  Per key
-// tile and query tile the tensor cores need 960 cycles for a key of 192 and a
-// value of 128 (12 MMAs of N = 96, 6 of N = 128), the special-function units
-// 768 for 128 x 96 exponentials at 16 a cycle, of which a quarter is moved to
-// the FMA pipe.  A softmax step takes longer than the MMAs of a tile from
-// start to end, so everything that can is taken off the path between two
-// steps of a query tile: its next scores are formed while its softmax runs
-// (the scores' columns are free as soon as they are in registers), and the
-// other query tile's MMAs fill what is left.
+// tile and query tile, for a key of 192 and a value of 128, shared memory gives
+// the operands of the scores (12 MMAs of N = 96 that read 7 KB each, at 128
+// bytes a cycle) in 672 cycles, P.V (6 MMAs of N = 128, P from TMEM) takes 384,
+// and the special-function units 768 for 128 x 96 exponentials at 16 a cycle.
+// A softmax step from start to end takes longer than the MMAs of a tile, so
+// everything that can is taken off the path between two steps of a query tile:
+// its next scores are formed while its softmax runs (the scores' columns are
+// free as soon as they are in registers), and the other query tile's MMAs fill
+// what is left.  Measured: 1150 cycles per key tile and query tile (1056 of
+// MMAs) in the middle of an 8K prompt; the whole call, causal, 128 heads, runs
+// at 1.38 PFLOP/s from a cold start and at 1.2 when repeated, at the power cap.
+// Forming a part of the exponentials on the FMA pipe makes the softmax shorter
+// and the call longer (8K prompt 2263 us without, 2321 with a quarter of them).
 //
 // TMEM (512 columns): outputs of the two query tiles (128 each), their scores
 // (96 each), and one tile of bf16 probabilities (48) that the two take turns
@@ -73,7 +78,6 @@ constexpr int kLaunchRegs = 168, kIssueRegs = 88, kSoftmaxRegs = 208;
 static_assert(kIssueRegs + 2 * kSoftmaxRegs <= 3 * kLaunchRegs, "register split");
 constexpr int kQBox = kTile * 128;                // 128 query rows x 64 bf16
 constexpr int kBox = kKeys * 128;                 // 96 keys x 64 bf16
-constexpr int kExpCycle = 4, kExpFma = 1;         // of four pairs of exponentials, one on the FMA pipe
 constexpr int kHeadGroup = 8;
 constexpr int kBarBytes = 1024;
 constexpr int kSmemMax = 227 * 1024;
@@ -177,38 +181,6 @@ __device__ __forceinline__ void tmem_ld_wait(float *r)
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// d = a * b on two fp32 lanes at once
-__device__ __forceinline__ void fmul2(float &dx, float &dy, float ax, float ay, float bx, float by)
-{
-    asm("{\n\t.reg .b64 a2, b2, d2;\n\tmov.b64 a2, {%2, %3};\n\tmov.b64 b2, {%4, %5};\n\t"
-        "mul.rn.f32x2 d2, a2, b2;\n\tmov.b64 {%0, %1}, d2;\n\t}"
-        : "=f"(dx), "=f"(dy)
-        : "f"(ax), "f"(ay), "f"(bx), "f"(by));
-}
-
-// 2^x of two values on the FMA pipe, for x <= 127: x = n + f with n the nearest
-// whole number (read from the low bits of x + 1.5 * 2^23), 2^f on [-1/2, 1/2]
-// by a quartic, scaled by 2^n.  Its coefficients minimise the relative error
-// for a constant term of 1: 2.9e-6, against the 2^-9 that P is rounded with
-// and within what the sum's fp32 additions lose.  x at or below -127 gives
-// exactly 0 (masked keys); NaN stays NaN.
-__device__ __forceinline__ void exp2_fma(float &e0, float &e1, float x0, float x1)
-{
-    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));      // -127
-    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
-    constexpr float kRound = 12582912.f;
-    float t0, t1, f0, f1, p0, p1;
-    fadd2(t0, t1, x0, x1, kRound, kRound);
-    fadd2(f0, f1, t0, t1, -kRound, -kRound);
-    ffma2(f0, f1, f0, f1, -1.f, -1.f, x0, x1);
-    ffma2(p0, p1, f0, f1, 0.009585382416844368f, 0.009585382416844368f, 0.05590662732720375f, 0.05590662732720375f);
-    ffma2(p0, p1, p0, p1, f0, f1, 0.24024038016796112f, 0.24024038016796112f);
-    ffma2(p0, p1, p0, p1, f0, f1, 0.6931241750717163f, 0.6931241750717163f);
-    ffma2(p0, p1, p0, p1, f0, f1, 1.f, 1.f);
-    fmul2(e0, e1, p0, p1, __uint_as_float((__float_as_uint(t0) << 23) + 0x3F800000u),
-          __uint_as_float((__float_as_uint(t1) << 23) + 0x3F800000u));
-}
 
 __device__ __forceinline__ int key_end(const PrefillArgs &a, const ragged::Tile &t, int rows_before, int rows)
 {
@@ -329,226 +301,226 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < 4) {
-    set_regs_down<kIssueRegs>();
-    if (warp == 0) {
-        // ---------------------------------------------------------------- TMA
-        if (lane == 0) {
-            uint32_t kn = 0, vn = 0;                     // key and value tiles loaded
-            uint32_t qn[2] = {0, 0};                     // query tiles loaded
-            auto load_q = [&](const Item &it, int i) {
-                if (qn[i] > 0 && !mbar_wait(&B.q_empty[i], (qn[i] - 1) & 1)) {
-                    ok = false;
-                    return;
-                }
-                ++qn[i];
-                mbar_arrive_expect_tx(&B.q_full[i], NKB * kQBox);
-                const int row = it.q0 + i * kTile;
+        set_regs_down<kIssueRegs>();
+        if (warp == 0) {
+            // ---------------------------------------------------------------- TMA
+            if (lane == 0) {
+                uint32_t kn = 0, vn = 0;                     // key and value tiles loaded
+                uint32_t qn[2] = {0, 0};                     // query tiles loaded
+                auto load_q = [&](const Item &it, int i) {
+                    if (qn[i] > 0 && !mbar_wait(&B.q_empty[i], (qn[i] - 1) & 1)) {
+                        ok = false;
+                        return;
+                    }
+                    ++qn[i];
+                    mbar_arrive_expect_tx(&B.q_full[i], NKB * kQBox);
+                    const int row = it.q0 + i * kTile;
 #pragma unroll
-                for (int b = 0; b < NKB; ++b) {
-                    unsigned char *dst = smem + (i * NKB + b) * kQBox;
-                    if (b < NKN)
-                        tma_load_3d(dst, &m.q, 64 * b, it.head, row, &B.q_full[i]);
-                    else
-                        tma_load_3d(dst, &m.qr, 0, it.head, row, &B.q_full[i]);
-                }
-            };
-            auto load_k = [&](const Item &it, int j) {
-                const int row = it.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = kn & 1;
-                if (kn >= 2 && !mbar_wait(&B.k_empty[st], ((kn >> 1) - 1) & 1)) {
-                    ok = false;
-                    return;
-                }
-                ++kn;
-                unsigned char *dst = smem + Lay::kKeysAt + st * Lay::kKeyTile;
-                mbar_arrive_expect_tx(&B.k_full[st], Lay::kKeyTile);
+                    for (int b = 0; b < NKB; ++b) {
+                        unsigned char *dst = smem + (i * NKB + b) * kQBox;
+                        if (b < NKN)
+                            tma_load_3d(dst, &m.q, 64 * b, it.head, row, &B.q_full[i]);
+                        else
+                            tma_load_3d(dst, &m.qr, 0, it.head, row, &B.q_full[i]);
+                    }
+                };
+                auto load_k = [&](const Item &it, int j) {
+                    const int row = it.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = kn & 1;
+                    if (kn >= 2 && !mbar_wait(&B.k_empty[st], ((kn >> 1) - 1) & 1)) {
+                        ok = false;
+                        return;
+                    }
+                    ++kn;
+                    unsigned char *dst = smem + Lay::kKeysAt + st * Lay::kKeyTile;
+                    mbar_arrive_expect_tx(&B.k_full[st], Lay::kKeyTile);
 #pragma unroll
-                for (int b = 0; b < NKB; ++b) {
-                    if (b < NKN)
-                        tma_load_3d(dst + b * kBox, &m.k, 64 * b, kvh, row, &B.k_full[st]);
-                    else
-                        tma_load_2d(dst + b * kBox, &m.kr, 0, row, &B.k_full[st]);
-                }
-            };
-            auto load_v = [&](const Item &it, int j) {
-                const int row = it.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = vn & 1;
-                if (vn >= 2 && !mbar_wait(&B.v_empty[st], ((vn >> 1) - 1) & 1)) {
-                    ok = false;
-                    return;
-                }
-                ++vn;
-                unsigned char *dst = smem + Lay::kValuesAt + st * Lay::kValueTile;
-                mbar_arrive_expect_tx(&B.v_full[st], Lay::kValueTile);
+                    for (int b = 0; b < NKB; ++b) {
+                        if (b < NKN)
+                            tma_load_3d(dst + b * kBox, &m.k, 64 * b, kvh, row, &B.k_full[st]);
+                        else
+                            tma_load_2d(dst + b * kBox, &m.kr, 0, row, &B.k_full[st]);
+                    }
+                };
+                auto load_v = [&](const Item &it, int j) {
+                    const int row = it.k0 + j * kKeys, kvh = it.head / a.heads_per_kv, st = vn & 1;
+                    if (vn >= 2 && !mbar_wait(&B.v_empty[st], ((vn >> 1) - 1) & 1)) {
+                        ok = false;
+                        return;
+                    }
+                    ++vn;
+                    unsigned char *dst = smem + Lay::kValuesAt + st * Lay::kValueTile;
+                    mbar_arrive_expect_tx(&B.v_full[st], Lay::kValueTile);
 #pragma unroll
-                for (int b = 0; b < NVB; ++b)
-                    tma_load_3d(dst + b * kBox, &m.v, 64 * b, kvh, row, &B.v_full[st]);
-            };
-            // items are handed out as CTAs get to them: the first by the block's
-            // number, then by a count that the plan kernel sets to 0
-            // (an item is looked up while the one before is loaded)
-            const int ntiles = a.header[0], items = ntiles * a.heads;
-            auto look_up = [&](int i) -> Item {
-                Item it{};
-                it.head = -1;
-                return i < items ? get_item(a, ntiles, i) : it;
-            };
-            Item next = look_up(blockIdx.x);
-            for (uint32_t given = 0; ok; ++given) {
-                const uint32_t slot = given % kItems;
-                const Item it = next;
-                if (given >= kItems && !mbar_wait(&B.item_empty[slot], (given / kItems - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                B.item[slot] = it;
-                mbar_arrive(&B.item_full[slot]);
-                if (it.head < 0)
-                    break;
-                const int after = (int)gridDim.x + atomicAdd(&a.header[1], 1);
-                const int n = max(it.n0, it.n1);
-                if (n == 0) {
-                    next = look_up(after);
-                    continue;
-                }
-                if (it.n0 > 0)
-                    load_q(it, 0);
-                if (ok)
-                    load_k(it, 0);
-                if (ok && it.n1 > 0)
-                    load_q(it, 1);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (j + 1 < n)
-                        load_k(it, j + 1);
-                    if (ok)
-                        load_v(it, j);
-                    if (j == 0)
+                    for (int b = 0; b < NVB; ++b)
+                        tma_load_3d(dst + b * kBox, &m.v, 64 * b, kvh, row, &B.v_full[st]);
+                };
+                // items are handed out as CTAs get to them: the first by the block's
+                // number, then by a count that the plan kernel sets to 0
+                // (an item is looked up while the one before is loaded)
+                const int ntiles = a.header[0], items = ntiles * a.heads;
+                auto look_up = [&](int i) -> Item {
+                    Item it{};
+                    it.head = -1;
+                    return i < items ? get_item(a, ntiles, i) : it;
+                };
+                Item next = look_up(blockIdx.x);
+                for (uint32_t given = 0; ok; ++given) {
+                    const uint32_t slot = given % kItems;
+                    const Item it = next;
+                    if (given >= kItems && !mbar_wait(&B.item_empty[slot], (given / kItems - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    B.item[slot] = it;
+                    mbar_arrive(&B.item_full[slot]);
+                    if (it.head < 0)
+                        break;
+                    const int after = (int)gridDim.x + atomicAdd(&a.header[1], 1);
+                    const int n = max(it.n0, it.n1);
+                    if (n == 0) {
                         next = look_up(after);
-                }
-            }
-            // every copy started here has landed before the CTA can exit
-            for (uint32_t st = 0; st < 2; ++st) {
-                // phase of the stage's last load
-                if (kn > st && !mbar_wait(&B.k_full[st], ((kn - 1 - st) >> 1) & 1))
-                    ok = false;
-                if (vn > st && !mbar_wait(&B.v_full[st], ((vn - 1 - st) >> 1) & 1))
-                    ok = false;
-                if (qn[st] > 0 && !mbar_wait(&B.q_full[st], (qn[st] - 1) & 1))
-                    ok = false;
-            }
-            if (!ok && a.err)
-                atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------- scores
-        const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);                           // K-major query boxes
-        const uint64_t kdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kKeysAt, 16, 1024, 2);  // K-major key boxes
-        uint32_t t = 0;                                  // key tiles of the items before
-        // phase bit i of query tile i: queries, scores taken to registers (the
-        // first tile's columns are free from the start)
-        uint32_t qpar = 0, fpar = 3;
-        for (const Item *it; ok && (it = next_item());) {
-            const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
-            done_item();
-            const int n = max(n0, n1);
-#pragma unroll 1
-            for (int x = 0; x < 2 * n; ++x) {
-                const int j = x >> 1, i = x & 1;
-                const int mine = i ? n1 : n0, other = i ? n0 : n1;
-                if (j >= mine)
-                    continue;
-                const uint32_t st = (t + j) & 1;
-                bool in = true;
-                if (i == 0 || j >= other)                // the first of the tile's uses
-                    in = mbar_wait(&B.k_full[st], ((t + j) >> 1) & 1);
-                if (j == 0) {
-                    in = in && mbar_wait(&B.q_full[i], (qpar >> i) & 1);
-                    qpar ^= 1u << i;
-                }
-                in = in && mbar_wait(&B.s_free[i], (fpar >> i) & 1);
-                fpar ^= 1u << i;
-                ok = __all_sync(0xffffffffu, in);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint64_t qd = qdesc + (uint64_t)(i * NKB * (kQBox >> 4));
-                const uint64_t kd = kdesc + (uint64_t)(st * (Lay::kKeyTile >> 4));
-#pragma unroll
-                for (int k = 0; k < 4 * NKB; ++k)
-                    elect_ss(tS + i * kKeys, qd + (k / 4) * (kQBox >> 4) + (k % 4) * 2,
-                             kd + (k / 4) * (kBox >> 4) + (k % 4) * 2, kIdescS, k ? 1u : 0u);
-                elect_commit(&B.s_full[i]);
-                if (i == 1 || j >= other)                // the last of the tile's uses
-                    elect_commit(&B.k_empty[st]);
-                if (j + 1 == mine)
-                    elect_commit(&B.q_empty[i]);
-            }
-            t += (uint32_t)n;
-        }
-        finish();
-    } else if (warp == 2) {
-        // ---------------------------------------------------------------- P.V
-        const uint64_t vdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kValuesAt, kBox, 1024, 2);  // N-major value boxes
-        uint32_t t = 0;                                  // value tiles of the items before
-        uint32_t ppar = 0;                               // phase bit i: probabilities of query tile i
-        for (const Item *it; ok && (it = next_item());) {
-            const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
-            const int nk = __shfl_sync(0xffffffffu, it->nk, 0);
-            done_item();
-            const int n = max(n0, n1);
-            // the first to store probabilities waits for all items before
-            if (n > 0)
-                elect_commit(&B.p_free[n0 > 0 ? 0 : 1]);
-#pragma unroll 1
-            for (int x = 0; x < 2 * n; ++x) {
-                const int j = x >> 1, i = x & 1;
-                const int mine = i ? n1 : n0, other = i ? n0 : n1;
-                if (j >= mine)
-                    continue;
-                const uint32_t st = (t + j) & 1;
-                bool in = true;
-                if (i == 0 || j >= other) {              // the first of the tile's uses
-                    in = mbar_wait(&B.v_full[st], ((t + j) >> 1) & 1);
-                    // value rows past the sequence are zeroed: their
-                    // probabilities are 0, and 0 * NaN would poison the output
-                    const int ntok = nk - j * kKeys;
-                    if (ntok < kKeys) {
-                        in = __all_sync(0xffffffffu, in);
-                        unsigned char *v0 = smem + Lay::kValuesAt + st * Lay::kValueTile;
-                        for (int idx = lane; in && idx < (kKeys - ntok) * 8 * NVB; idx += 32) {
-                            const int b = idx / ((kKeys - ntok) * 8), rem = idx % ((kKeys - ntok) * 8);
-                            *reinterpret_cast<uint4 *>(v0 + b * kBox + (ntok + rem / 8) * 128 + (rem % 8) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                        continue;
+                    }
+                    if (it.n0 > 0)
+                        load_q(it, 0);
+                    if (ok)
+                        load_k(it, 0);
+                    if (ok && it.n1 > 0)
+                        load_q(it, 1);
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (j + 1 < n)
+                            load_k(it, j + 1);
+                        if (ok)
+                            load_v(it, j);
+                        if (j == 0)
+                            next = look_up(after);
                     }
                 }
-                in = in && mbar_wait(&B.p_full[i], (ppar >> i) & 1);
-                ppar ^= 1u << i;
-                ok = __all_sync(0xffffffffu, in);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint64_t vd = vdesc + (uint64_t)(st * (Lay::kValueTile >> 4));
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    elect_ts(tO + i * kTile, tP + 8 * k, vd + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-                // who is next to store probabilities: the other query tile
-                // where it has this tile (1) or the next one (0) to work off,
-                // else this one while it has more; after the item's last, see
-                // the item's start
-                const int next = j + i < other ? i ^ 1 : j + 1 < mine ? i : -1;
-                if (next >= 0)
-                    elect_commit(&B.p_free[next]);
-                if (i == 1 || j >= other)                // the last of the tile's uses
-                    elect_commit(&B.v_empty[st]);
-                if (j + 1 == mine)
-                    elect_commit(&B.o_full[i]);
+                // every copy started here has landed before the CTA can exit
+                for (uint32_t st = 0; st < 2; ++st) {
+                    // phase of the stage's last load
+                    if (kn > st && !mbar_wait(&B.k_full[st], ((kn - 1 - st) >> 1) & 1))
+                        ok = false;
+                    if (vn > st && !mbar_wait(&B.v_full[st], ((vn - 1 - st) >> 1) & 1))
+                        ok = false;
+                    if (qn[st] > 0 && !mbar_wait(&B.q_full[st], (qn[st] - 1) & 1))
+                        ok = false;
+                }
+                if (!ok && a.err)
+                    atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
             }
-            t += (uint32_t)n;
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------- scores
+            const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);                           // K-major query boxes
+            const uint64_t kdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kKeysAt, 16, 1024, 2);  // K-major key boxes
+            uint32_t t = 0;                                  // key tiles of the items before
+            // phase bit i of query tile i: queries, scores taken to registers (the
+            // first tile's columns are free from the start)
+            uint32_t qpar = 0, fpar = 3;
+            for (const Item *it; ok && (it = next_item());) {
+                const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
+                done_item();
+                const int n = max(n0, n1);
+#pragma unroll 1
+                for (int x = 0; x < 2 * n; ++x) {
+                    const int j = x >> 1, i = x & 1;
+                    const int mine = i ? n1 : n0, other = i ? n0 : n1;
+                    if (j >= mine)
+                        continue;
+                    const uint32_t st = (t + j) & 1;
+                    bool in = true;
+                    if (i == 0 || j >= other)                // the first of the tile's uses
+                        in = mbar_wait(&B.k_full[st], ((t + j) >> 1) & 1);
+                    if (j == 0) {
+                        in = in && mbar_wait(&B.q_full[i], (qpar >> i) & 1);
+                        qpar ^= 1u << i;
+                    }
+                    in = in && mbar_wait(&B.s_free[i], (fpar >> i) & 1);
+                    fpar ^= 1u << i;
+                    ok = __all_sync(0xffffffffu, in);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t qd = qdesc + (uint64_t)(i * NKB * (kQBox >> 4));
+                    const uint64_t kd = kdesc + (uint64_t)(st * (Lay::kKeyTile >> 4));
+#pragma unroll
+                    for (int k = 0; k < 4 * NKB; ++k)
+                        elect_ss(tS + i * kKeys, qd + (k / 4) * (kQBox >> 4) + (k % 4) * 2,
+                                 kd + (k / 4) * (kBox >> 4) + (k % 4) * 2, kIdescS, k ? 1u : 0u);
+                    elect_commit(&B.s_full[i]);
+                    if (i == 1 || j >= other)                // the last of the tile's uses
+                        elect_commit(&B.k_empty[st]);
+                    if (j + 1 == mine)
+                        elect_commit(&B.q_empty[i]);
+                }
+                t += (uint32_t)n;
+            }
+            finish();
+        } else if (warp == 2) {
+            // ---------------------------------------------------------------- P.V
+            const uint64_t vdesc = smem_desc(smem_u32(smem) + (uint32_t)Lay::kValuesAt, kBox, 1024, 2);  // N-major value boxes
+            uint32_t t = 0;                                  // value tiles of the items before
+            uint32_t ppar = 0;                               // phase bit i: probabilities of query tile i
+            for (const Item *it; ok && (it = next_item());) {
+                const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
+                const int nk = __shfl_sync(0xffffffffu, it->nk, 0);
+                done_item();
+                const int n = max(n0, n1);
+                // the first to store probabilities waits for all items before
+                if (n > 0)
+                    elect_commit(&B.p_free[n0 > 0 ? 0 : 1]);
+#pragma unroll 1
+                for (int x = 0; x < 2 * n; ++x) {
+                    const int j = x >> 1, i = x & 1;
+                    const int mine = i ? n1 : n0, other = i ? n0 : n1;
+                    if (j >= mine)
+                        continue;
+                    const uint32_t st = (t + j) & 1;
+                    bool in = true;
+                    if (i == 0 || j >= other) {              // the first of the tile's uses
+                        in = mbar_wait(&B.v_full[st], ((t + j) >> 1) & 1);
+                        // value rows past the sequence are zeroed: their
+                        // probabilities are 0, and 0 * NaN would poison the output
+                        const int ntok = nk - j * kKeys;
+                        if (ntok < kKeys) {
+                            in = __all_sync(0xffffffffu, in);
+                            unsigned char *v0 = smem + Lay::kValuesAt + st * Lay::kValueTile;
+                            for (int idx = lane; in && idx < (kKeys - ntok) * 8 * NVB; idx += 32) {
+                                const int b = idx / ((kKeys - ntok) * 8), rem = idx % ((kKeys - ntok) * 8);
+                                *reinterpret_cast<uint4 *>(v0 + b * kBox + (ntok + rem / 8) * 128 + (rem % 8) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    in = in && mbar_wait(&B.p_full[i], (ppar >> i) & 1);
+                    ppar ^= 1u << i;
+                    ok = __all_sync(0xffffffffu, in);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t vd = vdesc + (uint64_t)(st * (Lay::kValueTile >> 4));
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        elect_ts(tO + i * kTile, tP + 8 * k, vd + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+                    // who is next to store probabilities: the other query tile
+                    // where it has this tile (1) or the next one (0) to work off,
+                    // else this one while it has more; after the item's last, see
+                    // the item's start
+                    const int next = j + i < other ? i ^ 1 : j + 1 < mine ? i : -1;
+                    if (next >= 0)
+                        elect_commit(&B.p_free[next]);
+                    if (i == 1 || j >= other)                // the last of the tile's uses
+                        elect_commit(&B.v_empty[st]);
+                    if (j + 1 == mine)
+                        elect_commit(&B.o_full[i]);
+                }
+                t += (uint32_t)n;
+            }
+            finish();
         }
-        finish();
-    }
     } else {
         set_regs_up<kSoftmaxRegs>();
         // ------------------------------------------------------------ softmax
@@ -618,14 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t pk[kKeys / 2];
 #pragma unroll
                 for (int x = 0; x < kKeys / 2; ++x) {
-                    float x0, x1, e0, e1;
+                    float x0, x1;
                     ffma2(x0, x1, s[2 * x], s[2 * x + 1], c, c, nm, nm);
-                    if (x % kExpCycle >= kExpCycle - kExpFma) {
-                        exp2_fma(e0, e1, x0, x1);
-                    } else {
-                        e0 = exp2_approx(x0);
-                        e1 = exp2_approx(x1);
-                    }
+                    const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
                     fadd2(sx[x & 3], sy[x & 3], sx[x & 3], sy[x & 3], e0, e1);
                     const __nv_bfloat162 v2 = __floats2bfloat162_rn(e0, e1);
                     pk[x] = *reinterpret_cast<const uint32_t *>(&v2);
