@@ -417,7 +417,8 @@ int kvattn_head_proj(const void *x, const void *w, void *y, int32_t out_dtype, i
  * (q_start stops there), BAD_LENGTH for a negative length (taken as 0).
  * PAGE_OUT_OF_RANGE: a page id outside [0, num_pages), in the table or the free
  * list; its tokens get slot -1.
- * All pointers 4-byte aligned; batch <= 16384, num_pages < 2^25.
+ * All pointers 4-byte aligned; batch <= 16384, num_pages < 2^25, max_tokens <=
+ * 2^30.
  */
 int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int32_t num_pages, int32_t max_tokens,
                         const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_pages,
@@ -480,12 +481,12 @@ int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cac
  * newest nq of the sequence's nk tokens); a query without keys gives out = 0,
  * lse = -inf.  causal = 0: every query attends every key.
  *
- * Strides in elements, {between tokens, between heads}; {0, 0} takes the dense
+ * Strides in elements, {between tokens, between heads}; 0 takes that of the dense
  * layout: q_nope [T][H][d_nope], q_rope [T][H][d_rope], out [T][H][d_v], and
  * head-major k [KH][max_kv_tokens][d_nope], v [KH][max_kv_tokens][d_v] (as
  * kvattn_expand_kv writes them); k_rope [T][d_rope] has a token stride only.
- * The last axis is contiguous; strides are multiples of 8; heads and tokens of
- * out do not overlap.  lse (may be NULL) is fp32 [max_q_tokens][H].  bf16
+ * The last axis is contiguous; strides are positive multiples of 8; out overlaps
+ * neither itself nor an input.  lse (may be NULL) is fp32 [max_q_tokens][H].  bf16
  * inputs; out bf16 (nearest even) or fp32.  d_nope and d_v multiples of 8 up to
  * 128, d_rope of 8 up to 64.
  * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded to

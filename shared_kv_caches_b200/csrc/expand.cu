@@ -492,7 +492,7 @@ extern "C" int kvattn_expand_workspace_size(int32_t variant, const kvattn_params
         return st;
     if (!bytes || max_kv_tokens < 0)
         return KVATTN_ERR_INVALID_ARG;
-    if (variant != KVATTN_MLA && variant != KVATTN_GLA)
+    if ((variant != KVATTN_MLA && variant != KVATTN_GLA) || max_kv_tokens > ragged::kMaxRows)
         return KVATTN_ERR_UNSUPPORTED;
     *bytes = ragged::kPlanHeader +
              (size_t)ragged::tile_capacity(max_kv_tokens, p->batch, kRows) * sizeof(ragged::Tile);

@@ -764,7 +764,8 @@ int validate_prefill(const kvattn_prefill_params *p)
     if (p->out_dtype != KVATTN_OUT_BF16 && p->out_dtype != KVATTN_OUT_FP32)
         return KVATTN_ERR_INVALID_ARG;
     if (p->d_nope % 8 || p->d_rope % 8 || p->d_v % 8 || p->d_nope > 128 || p->d_rope > 64 || p->d_v > 128 ||
-        p->batch > ragged::kMaxBatch || p->num_q_heads > 65535)
+        p->batch > ragged::kMaxBatch || p->num_q_heads > 65535 || p->max_q_tokens > ragged::kMaxRows ||
+        p->max_kv_tokens > ragged::kMaxRows)
         return KVATTN_ERR_UNSUPPORTED;
     const long long cap = ragged::tile_capacity(p->max_q_tokens, p->batch, kItemRows);
     if (cap * ((p->num_q_heads + kHeadGroup - 1) / kHeadGroup * kHeadGroup) > INT32_MAX / 2)

@@ -10,6 +10,7 @@ namespace ragged {
 
 constexpr int kThreads = 1024;           // threads of a block that sums over the requests
 constexpr int kMaxBatch = 16384;         // requests whose sums fit its shared memory
+constexpr int kMaxRows = INT32_MAX - 4096;   // rows of a batch: a tile past the last one still has a 32-bit number
 
 // Exclusive sums over a block of kThreads threads; the total in `sum`.
 // sh: 32 values of shared memory.

@@ -362,7 +362,7 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
     if (!cached_lens || !new_lens || !free_pages || !free_count || !block_table || !seq_lens || !free_left ||
         !q_start || (max_tokens > 0 && (!pos || !slots)))
         return KVATTN_ERR_INVALID_ARG;
-    if (batch > ragged::kMaxBatch || num_pages > INT32_MAX / kPage)
+    if (batch > ragged::kMaxBatch || num_pages > INT32_MAX / kPage || max_tokens > (1 << 30))
         return KVATTN_ERR_UNSUPPORTED;
     for (const void *p : {static_cast<const void *>(cached_lens), static_cast<const void *>(new_lens),
                           static_cast<const void *>(free_pages), static_cast<const void *>(free_count),

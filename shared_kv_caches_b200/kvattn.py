@@ -329,40 +329,44 @@ def kvattn_prefill(params, q_nope, q_rope, k_nope, k_rope, v, q_start, kv_start,
                                  float(sm_scale), out, lse, workspace, int(workspace_bytes), device_error, stream)
 
 
-def _check(t, dtype, dims, device, what):
-    """The tensor a helper was given: its type, its axes and its device."""
-    if t.dtype is not dtype or t.dim() != dims or t.device != device or device.type != "cuda":
-        raise ValueError(f"{what}: {dims}-d {dtype} on a CUDA device wanted ({device}), got {t.dim()}-d {t.dtype} on {t.device}")
+def _check(t, dtype, dims, index, what):
+    """The tensor a helper was given: its type, its axes and its CUDA device's
+    number; returns it."""
+    if t.dtype is not dtype or t.dim() != dims or t.get_device() != index or index < 0:
+        raise ValueError(f"{what}: {dims}-d {dtype} on CUDA device {index} wanted, got {t.dim()}-d {t.dtype} on {t.device}")
     return t
 
 
-def _dense(t, dtype, dims, device, what):
-    if not _check(t, dtype, dims, device, what).is_contiguous():
+def _dense(t, dtype, dims, index, what):
+    if not _check(t, dtype, dims, index, what).is_contiguous():
         raise ValueError(f"{what} is not contiguous")
     return t
 
 
-def _enqueue(what, device, fn, *args) -> None:
+def _last_axis(t, dtype, dims, index, what):
+    """The strides of a tensor whose last axis is contiguous."""
+    s = _check(t, dtype, dims, index, what).stride()
+    if s[-1] != 1 or 0 in s:
+        raise ValueError(f"{what}: the last axis is not contiguous, or an axis is broadcast")
+    return s
+
+
+def _enqueue(what, index, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, with that device
     current (a kernel runs on the device that is current at its launch)."""
-    import torch
-    index = device.index
-    if torch.cuda.current_device() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    from torch import _C, cuda
+    if cuda.current_device() == index:
+        st = fn(*args, _C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        with cuda.device(index):
+            st = fn(*args, _C._cuda_getCurrentRawStream(index))
     if st:
         raise KvattnError(st, what)
 
 
-def _error_word(t, device):
-    return None if t is None else _dense(t, _torch_int32(), 1, device, "device_error").data_ptr()
-
-
-def _torch_int32():
+def _error_word(t, index):
     import torch
-    return torch.int32
+    return None if t is None else _dense(t, torch.int32, 1, index, "device_error").data_ptr()
 
 
 def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_table, max_tokens, device_error=None,
@@ -373,7 +377,7 @@ def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_ta
     pos and slots.  inplace: seq_lens and free_left are cached_lens and
     free_count, updated (no new lengths are allocated)."""
     import torch
-    dev, i32 = cached_lens.device, torch.int32
+    dev, i32 = cached_lens.get_device(), torch.int32
     _dense(cached_lens, i32, 1, dev, "cached_lens")
     _dense(new_lens, i32, 1, dev, "new_lens")
     _dense(free_pages, i32, 1, dev, "free_pages")
@@ -385,7 +389,7 @@ def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_ta
         raise ValueError("cached_lens, new_lens and block_table have one row a request, free_count one value")
     # the outputs share one allocation, pos and slots in front (on 16 bytes)
     sizes = [n, n, B + 1, B + 1] if inplace else [n, n, B + 1, B + 1, B, 1]
-    r = torch.empty(sum(sizes), dtype=i32, device=dev)
+    r = torch.empty(sum(sizes), dtype=i32, device=cached_lens.device)
     pos = r.data_ptr()
     slots, q_start, kv_start, end = pos + 4 * n, pos + 8 * n, pos + 8 * n + 4 * B + 4, pos + 8 * n + 8 * B + 8
     if inplace:
@@ -404,7 +408,7 @@ def append_slots_tensor(variant, params, new_kv, pos, slots, kv_cache, rope_base
     """``kvattn_append_slots`` on tensors: new_kv bf16 [tokens][...], pos and
     slots int32 [tokens], kv_cache the pool (bf16, or e4m3 bytes)."""
     import torch
-    dev, variant = kv_cache.device, int(variant)
+    dev, variant = kv_cache.get_device(), int(variant)
     fp8 = params.cache_dtype == KVATTN_CACHE_FP8_E4M3
     n = _dense(slots, torch.int32, 1, dev, "slots").shape[0]
     _dense(new_kv, torch.bfloat16, new_kv.dim(), dev, "new_kv")
@@ -431,25 +435,23 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
     [H][max_kv_tokens][d_v] and k_rope [max_kv_tokens][d_rope] (None without a
     rope part)."""
     import torch
-    dev, bf16 = kv_cache.device, torch.bfloat16
-    H, dn, dr, n = params.num_q_heads, params.d_nope, params.d_rope, int(max_kv_tokens)
-    _dense(kv_cache, bf16, kv_cache.dim(), dev, "kv_cache")
-    _dense(w_uk, bf16, 3, dev, "w_uk")
-    _dense(w_uv, bf16, 3, dev, "w_uv")
-    _dense(kv_start, torch.int32, 1, dev, "kv_start")
-    d_k, d_v = w_uk.shape[1], w_uv.shape[2]
-    if w_uk.shape != (H, d_k, dn) or w_uv.shape != (H, dn, d_v) or kv_start.shape[0] != params.batch + 1:
-        raise ValueError("w_uk is [H][d_k][d_nope], w_uv [H][d_nope][d_v], kv_start [batch + 1]")
-    if kv_cache.numel() != params.num_pages * 64 * (params.num_kv * dn + dr):
+    dev, bf16, at = kv_cache.get_device(), torch.bfloat16, kv_cache.device
+    H, dn, dr, B, n = params.num_q_heads, params.d_nope, params.d_rope, params.batch, int(max_kv_tokens)
+    if _dense(kv_cache, bf16, kv_cache.dim(), dev, "kv_cache").numel() != params.num_pages * 64 * (
+            params.num_kv * dn + dr):
         raise ValueError("kv_cache is not the pool that params describe")
+    h1, d_k, c1 = _dense(w_uk, bf16, 3, dev, "w_uk").shape
+    h2, c2, d_v = _dense(w_uv, bf16, 3, dev, "w_uv").shape
+    if h1 != H or h2 != H or c1 != dn or c2 != dn or _dense(kv_start, torch.int32, 1, dev, "kv_start").numel() != B + 1:
+        raise ValueError("w_uk is [H][d_k][d_nope], w_uv [H][d_nope][d_v], kv_start [batch + 1]")
     if block_table is not None and _dense(block_table, torch.int32, 2, dev, "block_table").shape != (
-            params.batch, params.max_pages_per_seq):
+            B, params.max_pages_per_seq):
         raise ValueError("block_table is [batch][max_pages_per_seq]")
-    k = torch.empty((H, n, d_k), dtype=bf16, device=dev)
-    v = torch.empty((H, n, d_v), dtype=bf16, device=dev)
-    k_rope = torch.empty((n, dr), dtype=bf16, device=dev) if dr else None
+    k = torch.empty((H, n, d_k), dtype=bf16, device=at)
+    v = torch.empty((H, n, d_v), dtype=bf16, device=at)
+    k_rope = torch.empty((n, dr), dtype=bf16, device=at) if dr else None
     if n:
-        ws = torch.empty(kvattn_expand_workspace_size(variant, params, n), dtype=torch.uint8, device=dev)
+        ws = torch.empty(kvattn_expand_workspace_size(variant, params, n), dtype=torch.uint8, device=at)
         _enqueue("kvattn_expand_kv", dev, load().kvattn_expand_kv, int(variant), ctypes.byref(params),
                  kv_cache.data_ptr(), _ptr(block_table), kv_start.data_ptr(), n, d_k, d_v, w_uk.data_ptr(),
                  w_uv.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_rope), ws.data_ptr(), ws.numel(),
@@ -466,38 +468,42 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
     [B + 1].  Returns out [T][H][d_v] and lse [T][H]; rows past the last
     sequence are left as they were."""
     import torch
-    dev, bf16 = q_nope.device, torch.bfloat16
+    dev, bf16, at = q_nope.get_device(), torch.bfloat16, q_nope.device
     rope = q_rope is not None
     if rope != (k_rope is not None):
         raise ValueError("q_rope and k_rope go together")
-    for t, dims, what in ((q_nope, 3, "q_nope"), (k, 3, "k"), (v, 3, "v")) + (
-            ((q_rope, 3, "q_rope"), (k_rope, 2, "k_rope")) if rope else ()):
-        if _check(t, bf16, dims, dev, what).stride(-1) != 1:
-            raise ValueError(f"{what}: the last axis is not contiguous")
-    B = _dense(q_start, torch.int32, 1, dev, "q_start").shape[0] - 1
-    _dense(kv_start, torch.int32, 1, dev, "kv_start")
+    qs = _last_axis(q_nope, bf16, 3, dev, "q_nope")
+    ks = _last_axis(k, bf16, 3, dev, "k")
+    vs = _last_axis(v, bf16, 3, dev, "v")
     (T, H, dn), (KH, Tk, d_v) = q_nope.shape, v.shape
-    dr = q_rope.shape[2] if rope else 0
-    if k.shape != (KH, Tk, dn) or kv_start.shape[0] != B + 1 or (
-            rope and (q_rope.shape != (T, H, dr) or k_rope.shape != (Tk, dr))):
+    B = _dense(q_start, torch.int32, 1, dev, "q_start").numel() - 1
+    if k.shape != (KH, Tk, dn) or _dense(kv_start, torch.int32, 1, dev, "kv_start").numel() != B + 1:
         raise ValueError("the shapes of queries, keys, values and starts do not fit together")
+    dr, rs, krs = 0, (0, 0), 0
+    if rope:
+        rs, krs = _last_axis(q_rope, bf16, 3, dev, "q_rope"), _last_axis(k_rope, bf16, 2, dev, "k_rope")[0]
+        dr = q_rope.shape[2]
+        if q_rope.shape != (T, H, dr) or k_rope.shape != (Tk, dr):
+            raise ValueError("the shapes of queries, keys, values and starts do not fit together")
+    dtype = torch.float32 if out_fp32 else bf16
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=torch.float32 if out_fp32 else bf16, device=dev)
-    elif _check(out, torch.float32 if out_fp32 else bf16, 3, dev, "out").shape != (T, H, d_v) or out.stride(-1) != 1:
-        raise ValueError("out is [T][H][d_v] with a contiguous last axis")
+        out, os = torch.empty((T, H, d_v), dtype=dtype, device=at), (0, 0)
+    else:
+        os = _last_axis(out, dtype, 3, dev, "out")
+        if out.shape != (T, H, d_v):
+            raise ValueError("out is [T][H][d_v]")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=at)
     elif _dense(lse, torch.float32, 2, dev, "lse").shape != (T, H):
         raise ValueError("lse is [T][H]")
     if T:
-        def steps(t, token=0, head=1):
-            # an axis of one element has no stride of its own
-            return (t.stride(token) if t.shape[token] > 1 else 0, t.stride(head) if t.shape[head] > 1 else 0)
+        # an axis of one element has no stride of its own
+        t1, h1, k1, kh1 = T > 1, H > 1, Tk > 1, KH > 1
         p = kvattn_prefill_params(B, H, KH, dn, dr, d_v, T, Tk, 1 if causal else 0,
-                                  KVATTN_OUT_FP32 if out_fp32 else KVATTN_OUT_BF16, steps(q_nope),
-                                  steps(q_rope) if rope else (0, 0), steps(k, 1, 0), steps(v, 1, 0), steps(out),
-                                  k_rope.stride(0) if rope and Tk > 1 else 0)
-        ws = torch.empty(kvattn_prefill_workspace_size(p), dtype=torch.uint8, device=dev)
+                                  KVATTN_OUT_FP32 if out_fp32 else KVATTN_OUT_BF16, (qs[0] * t1, qs[1] * h1),
+                                  (rs[0] * t1, rs[1] * h1), (ks[1] * k1, ks[0] * kh1), (vs[1] * k1, vs[0] * kh1),
+                                  (os[0] * t1, os[1] * h1), krs * k1)
+        ws = torch.empty(kvattn_prefill_workspace_size(p), dtype=torch.uint8, device=at)
         _enqueue("kvattn_prefill", dev, load().kvattn_prefill, ctypes.byref(p), q_nope.data_ptr(), _ptr(q_rope),
                  k.data_ptr(), _ptr(k_rope), v.data_ptr(), q_start.data_ptr(), kv_start.data_ptr(), sm_scale,
                  out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _error_word(device_error, dev))

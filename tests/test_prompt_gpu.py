@@ -486,6 +486,31 @@ def test_prefill_strided_views(dev):
     assert bool((wide[:, H] == 3.0).all()) and bool((wide[..., dv:] == 3.0).all())
 
 
+def test_prefill_one_head_one_token_and_broadcast_axes(dev):
+    """Axes of one element may have any stride; a broadcast axis is refused."""
+    import torch
+    rng = np.random.default_rng(21)
+    x = prefill_case(rng, 1, 1, 64, 0, 64, [1], [1], slack=0)
+    t = {k: None if v is None else up(v, dev) for k, v in x.items()}
+    q = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device=dev)
+    q[:, 1:2] = t["q"]
+    got = K.prefill_tensors(q[:, 1:2].as_strided((1, 1, 64), (7, 3, 1), 64), None, t["k"], None, t["v"], i32([0, 1], dev),
+                            i32([0, 1], dev), 0.1)
+    check_prefill(got, x, [1], [1], 0.1, True)
+    with pytest.raises(ValueError):
+        K.prefill_tensors(t["q"].expand(1, 4, 64), None, t["k"].expand(4, 1, 64), None, t["v"].expand(4, 1, 64),
+                          i32([0, 1], dev), i32([0, 1], dev), 0.1)
+
+
+def test_prefill_without_keys(dev):
+    """No key rows at all: zeros and -inf for every query."""
+    import torch
+    z = torch.zeros(2, 0, 64, dtype=torch.bfloat16, device=dev)
+    got = K.prefill_tensors(torch.ones(200, 2, 64, dtype=torch.bfloat16, device=dev), None, z, None, z, i32([0, 150, 200], dev),
+                            i32([0, 0, 0], dev), 0.1)
+    assert bool((got["out"] == 0).all()) and bool(torch.isinf(got["lse"]).all())
+
+
 def test_prefill_leaves_rows_past_the_last_sequence(dev):
     import torch
     rng = np.random.default_rng(14)

@@ -31,7 +31,7 @@ def tables(batch=4, mpps=8, pages=100, tokens=64, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=0), INVALID), (dict(mpps=0), INVALID), (dict(pages=0), INVALID), (dict(tokens=-1), INVALID),
-    (dict(batch=16385), UNSUPPORTED), (dict(pages=1 << 25), UNSUPPORTED),
+    (dict(batch=16385), UNSUPPORTED), (dict(pages=1 << 25), UNSUPPORTED), (dict(tokens=(1 << 30) + 1), UNSUPPORTED),
     (dict(pos=None), INVALID), (dict(slots=None), INVALID), (dict(slots=FAKE + 2), MISALIGNED), (dict(err=FAKE + 1), MISALIGNED),
 ])
 def test_tables_refusals(lib, kw, status):
@@ -80,7 +80,7 @@ def expand(variant=K.KVATTN_MLA, n=500, d_k=128, d_v=128, ws_bytes=1 << 30, err=
     (dict(d_v=60), UNSUPPORTED), (dict(d_nope=72), UNSUPPORTED), (dict(ws_bytes=100), SMALL),
     (dict(variant=K.KVATTN_MLRA), UNSUPPORTED), (dict(variant=K.KVATTN_GQA, d_rope=0), UNSUPPORTED),
     (dict(ptr=dict(ws=FAKE + 16)), MISALIGNED), (dict(err=FAKE + 2), MISALIGNED), (dict(n=0), 0),
-    (dict(batch=16385), UNSUPPORTED), (dict(page_size=32), UNSUPPORTED),
+    (dict(batch=16385), UNSUPPORTED), (dict(page_size=32), UNSUPPORTED), (dict(n=2 ** 31 - 2), UNSUPPORTED),
 ])
 def test_expand_refusals(lib, kw, status):
     assert expand(**kw) == status
@@ -122,6 +122,7 @@ def prefill(scale=0.1, lse=FAKE, err=None, ws_bytes=1 << 30, ptr=None, **kw):
     (dict(d_nope=100), UNSUPPORTED), (dict(d_nope=256), UNSUPPORTED), (dict(d_rope=72), UNSUPPORTED), (dict(d_v=136), UNSUPPORTED),
     (dict(batch=16385), UNSUPPORTED), (dict(max_q_tokens=2 ** 31 - 1, num_q_heads=65535, num_kv_heads=1), UNSUPPORTED),
     (dict(ws_bytes=255), SMALL), (dict(lse=FAKE + 2), MISALIGNED), (dict(err=FAKE + 2), MISALIGNED),
+    (dict(max_q_tokens=2 ** 31 - 2, num_q_heads=1, num_kv_heads=1), UNSUPPORTED), (dict(max_kv_tokens=2 ** 31 - 2), UNSUPPORTED),
     (dict(k_stride=(4, 128)), INVALID), (dict(v_stride=(-8, 128)), INVALID), (dict(out_stride=(1 << 38, 8)), INVALID),
     (dict(q_rope_stride=(12, 8)), INVALID), (dict(k_rope_stride=20), INVALID), (dict(max_q_tokens=0), 0),
 ])
