@@ -110,11 +110,14 @@ struct Layout {
     static_assert(kBytes <= kSmemMax, "shared memory");
 };
 
-// A work item: a tile of the list, a head, and the key tiles of its two query tiles.
+// A work item: a tile of the list, a head, and the keys of its two query tiles.
 struct Item {
     int32_t q0, nq, k0, nk, lim0;                 // as in ragged::Tile
     int32_t head;                                 // -1: no more items
-    int32_t n0, n1;
+    int32_t end0, end1;                           // keys that the last row of each query tile attends
+
+    __device__ __forceinline__ int tiles0() const { return (end0 + kKeys - 1) / kKeys; }
+    __device__ __forceinline__ int tiles1() const { return (end1 + kKeys - 1) / kKeys; }
 };
 
 // The items that the TMA thread hands out stand here until all have read them.
@@ -220,8 +223,8 @@ __device__ __forceinline__ Item get_item(const PrefillArgs &a, int ntiles, int i
     it.nk = t.nk;
     it.lim0 = t.lim0;
     it.head = g * kHeadGroup + r % hc;
-    it.n0 = (key_end(a, t, 0, min(t.nq, kTile)) + kKeys - 1) / kKeys;
-    it.n1 = (key_end(a, t, kTile, t.nq - kTile) + kKeys - 1) / kKeys;
+    it.end0 = key_end(a, t, 0, min(t.nq, kTile));
+    it.end1 = key_end(a, t, kTile, t.nq - kTile);
     return it;
 }
 
@@ -376,16 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (it.head < 0)
                         break;
                     const int after = (int)gridDim.x + atomicAdd(&a.header[1], 1);
-                    const int n = max(it.n0, it.n1);
+                    const int n0 = it.tiles0(), n1 = it.tiles1(), n = max(n0, n1);
                     if (n == 0) {
                         next = look_up(after);
                         continue;
                     }
-                    if (it.n0 > 0)
+                    if (n0 > 0)
                         load_q(it, 0);
                     if (ok)
                         load_k(it, 0);
-                    if (ok && it.n1 > 0)
+                    if (ok && n1 > 0)
                         load_q(it, 1);
                     for (int j = 0; ok && j < n; ++j) {
                         if (j + 1 < n)
@@ -419,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // first tile's columns are free from the start)
             uint32_t qpar = 0, fpar = 3;
             for (const Item *it; ok && (it = next_item());) {
-                const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
+                const int end0 = __shfl_sync(0xffffffffu, it->end0, 0), end1 = __shfl_sync(0xffffffffu, it->end1, 0);
                 done_item();
-                const int n = max(n0, n1);
+                const int n0 = (end0 + kKeys - 1) / kKeys, n1 = (end1 + kKeys - 1) / kKeys, n = max(n0, n1);
 #pragma unroll 1
                 for (int x = 0; x < 2 * n; ++x) {
                     const int j = x >> 1, i = x & 1;
@@ -442,12 +445,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok)
                         break;
                     tc_fence_after();
+                    // the last tile's scores only as far as a row attends (in
+                    // steps of 16; what stands in the other columns is masked)
+                    const int keys = min(kKeys, ((i ? end1 : end0) - j * kKeys + 15) & ~15);
+                    const uint32_t idesc = (kIdescS & ~(0x3Fu << 17)) | (uint32_t)(keys >> 3) << 17;
                     const uint64_t qd = qdesc + (uint64_t)(i * NKB * (kQBox >> 4));
                     const uint64_t kd = kdesc + (uint64_t)(st * (Lay::kKeyTile >> 4));
 #pragma unroll
                     for (int k = 0; k < 4 * NKB; ++k)
                         elect_ss(tS + i * kKeys, qd + (k / 4) * (kQBox >> 4) + (k % 4) * 2,
-                                 kd + (k / 4) * (kBox >> 4) + (k % 4) * 2, kIdescS, k ? 1u : 0u);
+                                 kd + (k / 4) * (kBox >> 4) + (k % 4) * 2, idesc, k ? 1u : 0u);
                     elect_commit(&B.s_full[i]);
                     if (i == 1 || j >= other)                // the last of the tile's uses
                         elect_commit(&B.k_empty[st]);
@@ -463,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t t = 0;                                  // value tiles of the items before
             uint32_t ppar = 0;                               // phase bit i: probabilities of query tile i
             for (const Item *it; ok && (it = next_item());) {
-                const int n0 = __shfl_sync(0xffffffffu, it->n0, 0), n1 = __shfl_sync(0xffffffffu, it->n1, 0);
+                const int end0 = __shfl_sync(0xffffffffu, it->end0, 0), end1 = __shfl_sync(0xffffffffu, it->end1, 0);
                 const int nk = __shfl_sync(0xffffffffu, it->nk, 0);
                 done_item();
-                const int n = max(n0, n1);
+                const int n0 = (end0 + kKeys - 1) / kKeys, n1 = (end1 + kKeys - 1) / kKeys, n = max(n0, n1);
                 // the first to store probabilities waits for all items before
                 if (n > 0)
                     elect_commit(&B.p_free[n0 > 0 ? 0 : 1]);
@@ -504,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t vd = vdesc + (uint64_t)(st * (Lay::kValueTile >> 4));
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        elect_ts(tO + i * kTile, tP + 8 * k, vd + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+                        if (j * kKeys + 16 * k < (i ? end1 : end0))
+                            elect_ts(tO + i * kTile, tP + 8 * k, vd + (uint64_t)(k * 128), kIdescPV,
+                                     (j > 0 || k > 0) ? 1u : 0u);
                     // who is next to store probabilities: the other query tile
                     // where it has this tile (1) or the next one (0) to work off,
                     // else this one while it has more; after the item's last, see
@@ -533,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c = a.scale_log2;
         uint32_t sn = 0, on = 0;                         // score tiles and outputs taken
         for (const Item *it; ok && (it = next_item());) {
-            const int n = i ? it->n1 : it->n0;
+            const int n = i ? it->tiles1() : it->tiles0();
             const int lim = a.causal ? min(it->nk, it->lim0 + row) : it->nk;
             const int lim_first = __shfl_sync(0xffffffffu, lim, 0);     // limits grow with the row
             float m_ref = -INFINITY, l = 0.f;
