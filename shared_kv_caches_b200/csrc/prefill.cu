@@ -92,7 +92,8 @@ struct PrefillArgs {
     int d_v, out_fp32, causal;
     int wide;                                     // output rows start on 32 bytes
     long long out_token_stride, out_head_stride;
-    float scale_log2;
+    float scale_log2;                             // of the scale's magnitude
+    uint32_t negate;                              // a negative scale: the MMAs take -q (the instruction descriptor's bit)
 };
 
 struct Maps {
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the last tile's scores only as far as a row attends (in
                     // steps of 16; what stands in the other columns is masked)
                     const int keys = min(kKeys, ((i ? end1 : end0) - j * kKeys + 15) & ~15);
-                    const uint32_t idesc = (kIdescS & ~(0x3Fu << 17)) | (uint32_t)(keys >> 3) << 17;
+                    const uint32_t idesc = (kIdescS & ~(0x3Fu << 17)) | (uint32_t)(keys >> 3) << 17 | a.negate;
                     const uint64_t qd = qdesc + (uint64_t)(i * NKB * (kQBox >> 4));
                     const uint64_t kd = kdesc + (uint64_t)(st * (Lay::kKeyTile >> 4));
 #pragma unroll
@@ -546,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lim = a.causal ? min(it->nk, it->lim0 + row) : it->nk;
             const int lim_first = __shfl_sync(0xffffffffu, lim, 0);     // limits grow with the row
             float m_ref = -INFINITY, l = 0.f;
-            const float none = c >= 0.f ? -INFINITY : INFINITY;
             for (int j = 0; j < n; ++j) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&B.s_full[i], sn & 1));
                 if (!ok)
@@ -555,36 +555,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int nvalid = lim - j * kKeys;
                 const bool partial = lim_first - j * kKeys < kKeys;
-                // the next third is on its way while a third's maximum is taken
-                float s[kKeys];
-                float mx[3];
-                tmem_ld32_start(s_addr, s);
+                float s[kKeys], mx[3];
+#pragma unroll
+                for (int x = 0; x < kKeys; x += 32)
+                    tmem_ld32_start(s_addr + x, s + x);
+#pragma unroll
+                for (int x = 0; x < kKeys; x += 32)
+                    tmem_ld_wait(s + x);
+                // the scores are in registers: the next ones may come
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&B.s_free[i]);
 #pragma unroll
                 for (int x = 0; x < kKeys; x += 32) {
-                    tmem_ld_wait(s + x);
-                    if (x + 32 < kKeys) {
-                        tmem_ld32_start(s_addr + x + 32, s + x + 32);
-                    } else {
-                        // the scores are in registers: the next ones may come
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&B.s_free[i]);
-                    }
-                    // raw scores: the scale is folded into the exponent's FMA;
-                    // for a negative scale the row's maximum is at the lowest
+                    // raw scores: the scale is folded into the exponent's FMA
                     if (partial) {
 #pragma unroll
                         for (int y = x; y < x + 32; ++y)
-                            s[y] = y < nvalid ? s[y] : none;
+                            s[y] = y < nvalid ? s[y] : -INFINITY;
                     }
-                    if (c >= 0.f)
-                        mx[x / 32] = reduce_extreme<true, 32>(s + x);
-                    else
-                        mx[x / 32] = -reduce_extreme<false, 32>(s + x);
+                    mx[x / 32] = reduce_extreme<true, 32>(s + x);
                 }
                 const float e = latent::fmax3(mx[0], mx[1], mx[2]);
-                const float mt = e == -INFINITY ? -INFINITY : fabsf(c) * e;
+                const float mt = e == -INFINITY ? -INFINITY : c * e;
                 float alpha = 1.f;
                 bool rescale = false;
                 if (mt > m_ref + kRescaleThreshold) {
@@ -884,7 +878,8 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     a.out_head_stride = so[1];
     // masked scores are infinite, so a scale of 0 (every key weighs the same)
     // is taken as one too small to show in any weight
-    a.scale_log2 = sm_scale == 0.f ? 1e-30f : sm_scale * 1.4426950408889634f;
+    a.scale_log2 = sm_scale == 0.f ? 1e-30f : fabsf(sm_scale) * 1.4426950408889634f;
+    a.negate = sm_scale < 0.f ? 1u << 13 : 0u;
     c.most_items = pa.capacity * H;
 
     const int nkn = (p->d_nope + 63) / 64, nvb = (p->d_v + 63) / 64;
