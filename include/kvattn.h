@@ -456,8 +456,11 @@ int kvattn_append_slots(int32_t variant, const kvattn_params *p, const void *new
  *   k_rope[kv_start[b] + j]    = the cached k^R   bf16 [max_kv_tokens][d_rope]
  * fp32 accumulation, one rounding to bf16 (nearest even).  Weights as for
  * kvattn_head_proj: w_uk bf16 [H][d_k][d_nope], w_uv bf16 [H][d_nope][d_v].
- * MLA and GLA (p: the cache geometry; batch = sequences, block_table as for
- * decode; p->q_len and the split fields are not used).  d_nope a multiple of
+ * MLRA: every head has keys and values of each branch's latent; w_uk is
+ * [H][d_k][R*d_nope] (the branch blocks side by side), w_uv [H][R*d_nope][d_v]
+ * (stacked), k_nope and v have H*R blocks, block h*R + r of head h and branch r.
+ * p: the cache geometry; batch = sequences, block_table as for decode;
+ * p->q_len and the split fields are not used.  d_nope a multiple of
  * 64; d_k and d_v multiples of 8, at most 128.  A page id outside
  * [0, num_pages) sets KVATTN_DEVERR_PAGE_OUT_OF_RANGE; its tokens' keys and
  * values are 0.  k_rope may be NULL when d_rope == 0.
@@ -477,12 +480,16 @@ int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cac
  * key rows [kv_start[b], kv_start[b + 1]); head h reads key head h / (H / KH):
  *   s_ij = sm_scale * (q_nope[i][h] . k_nope[h'][j] + q_rope[i][h] . k_rope[j])
  *   out[i][h] = sum_j softmax_j(s_ij) v[h'][j],  lse[i][h] = ln sum_j exp(s_ij)
+ * num_q_nope_heads QH < H: heads share q_nope, head h reads q_nope head
+ * h / (H / QH).  MLRA in the expanded form is H = KH = heads * branches with QH =
+ * heads; out holds the branch outputs side by side (as kvattn_decode with
+ * branch_out does) and their sum is the layer's output.
  * causal = 1: query i of nq attends keys j <= i + nk - nq (the chunk is the
  * newest nq of the sequence's nk tokens); a query without keys gives out = 0,
  * lse = -inf.  causal = 0: every query attends every key.
  *
  * Strides in elements, {between tokens, between heads}; 0 takes that of the dense
- * layout: q_nope [T][H][d_nope], q_rope [T][H][d_rope], out [T][H][d_v], and
+ * layout: q_nope [T][QH][d_nope], q_rope [T][H][d_rope], out [T][H][d_v], and
  * head-major k [KH][max_kv_tokens][d_nope], v [KH][max_kv_tokens][d_v] (as
  * kvattn_expand_kv writes them); k_rope [T][d_rope] has a token stride only.
  * The last axis is contiguous; strides are positive multiples of 8; out overlaps
@@ -508,6 +515,7 @@ typedef struct {
     int32_t max_kv_tokens;     /* rows of k_nope, k_rope and v (>= kv_start[batch]) */
     int32_t causal;            /* 0 or 1 */
     int32_t out_dtype;         /* kvattn_out_dtype */
+    int32_t num_q_nope_heads;  /* QH, divides H; 0 = H */
     int64_t q_nope_stride[2];
     int64_t q_rope_stride[2];
     int64_t k_stride[2];

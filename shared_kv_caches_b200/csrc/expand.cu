@@ -117,7 +117,7 @@ struct ExpandArgs {
     const __nv_bfloat16 *cache;
     __nv_bfloat16 *k, *v, *k_rope;
     int32_t *err;
-    int heads, heads_per_group, groups, pairs_per_group, d_c, d_k, d_v, d_rope, row;
+    int heads, heads_per_group, groups, branches, pairs_per_group, d_c, d_k, d_v, d_rope, row;
     int mpps, num_pages, max_kv;
 };
 
@@ -296,7 +296,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 fresh = w.last_of_latents();
-                const int h = w.group * a.heads_per_group + 2 * w.pair + rank;
+                // MLRA: the branch's columns of every head's weight; else the group's heads
+                const int h = (a.branches > 1 ? 0 : w.group * a.heads_per_group) + 2 * w.pair + rank;
+                const int c0 = a.branches > 1 ? w.group * a.d_c : 0;
                 for (int kind = 0; ok && kind < 2; ++kind)
                     for (int c = 0; c < chunks; ++c, ++nb) {
                         const uint32_t st = nb % stages;
@@ -309,10 +311,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (rank == 0)
                             mbar_arrive_expect_tx(&B.b_full[st], 2 * kBox);
                         if (kind == 0) {
-                            pair_load_3d(dst, &kmap, c * kChunk, 0, h, bar, policy);
+                            pair_load_3d(dst, &kmap, c0 + c * kChunk, 0, h, bar, policy);
                         } else {
-                            pair_load_3d(dst, &vmap, 0, c * kChunk, h, bar, policy);
-                            pair_load_3d(dst + kBox / 2, &vmap, 64, c * kChunk, h, bar, policy);
+                            pair_load_3d(dst, &vmap, 0, c0 + c * kChunk, h, bar, policy);
+                            pair_load_3d(dst + kBox / 2, &vmap, 64, c0 + c * kChunk, h, bar, policy);
                         }
                     }
             }
@@ -405,7 +407,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int q0 = t.q0, nq = t.nq;
             const bool whole = (warp & 3) * 32 + 32 <= nq;
             const int heads = min(2, a.heads_per_group - 2 * w.pair);
-            const int h = w.group * a.heads_per_group + 2 * w.pair;
+            // output block of head p of the pair: h0 + p * step
+            const int step = a.branches;
+            const int h0 = step > 1 ? 2 * w.pair * step + w.group : w.group * a.heads_per_group + 2 * w.pair;
 #pragma unroll 1
             for (int kind = 0; kind < 2; ++kind, ++nd) {
                 const uint32_t buf = nd & 1;
@@ -414,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 tc_fence_after();
                 const int width = kind ? a.d_v : a.d_k;
-                __nv_bfloat16 *const rows = (kind ? a.v : a.k) + ((long long)h * a.max_kv + q0 + r0) * width;
+                __nv_bfloat16 *const rows = (kind ? a.v : a.k) + ((long long)h0 * a.max_kv + q0 + r0) * width;
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 64) {
                     uint32_t r[64];
@@ -451,10 +455,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0)
-                            tma_store_3d(kind ? &vout : &kout, c & 64, q0 + (warp & 3) * 32, h + (c >> 7), box,
+                            tma_store_3d(kind ? &vout : &kout, c & 64, q0 + (warp & 3) * 32, h0 + (c >> 7) * step, box,
                                          policy);
                     } else if (r0 < nq) {
-                        __nv_bfloat16 *const out = rows + (long long)(c >> 7) * a.max_kv * width + (c & 64);
+                        __nv_bfloat16 *const out = rows + (long long)((c >> 7) * step) * a.max_kv * width + (c & 64);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             if ((c & 64) + 8 * i < width)
@@ -492,7 +496,7 @@ extern "C" int kvattn_expand_workspace_size(int32_t variant, const kvattn_params
         return st;
     if (!bytes || max_kv_tokens < 0)
         return KVATTN_ERR_INVALID_ARG;
-    if ((variant != KVATTN_MLA && variant != KVATTN_GLA) || max_kv_tokens > ragged::kMaxRows)
+    if (!pr.latent || max_kv_tokens > ragged::kMaxRows)
         return KVATTN_ERR_UNSUPPORTED;
     *bytes = ragged::kPlanHeader +
              (size_t)ragged::tile_capacity(max_kv_tokens, p->batch, kRows) * sizeof(ragged::Tile);
@@ -532,6 +536,8 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto swz = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap cm, km, vm, ko, vo;
+    // latent columns that a head's weights have, and blocks of keys and values there are
+    const cuuint64_t cols = (cuuint64_t)(pr.mlra ? pr.NU : 1) * pr.dn, blocks = (cuuint64_t)pr.HU;
     {
         const cuuint64_t dims[2] = {(cuuint64_t)pr.row, (cuuint64_t)pr.num_pages * kPage};
         const cuuint64_t strides[1] = {(cuuint64_t)pr.row * 2};
@@ -540,22 +546,22 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
             return KVATTN_ERR_UNSUPPORTED;
     }
     {
-        const cuuint64_t dims[3] = {(cuuint64_t)pr.dn, (cuuint64_t)d_k, (cuuint64_t)pr.H};
-        const cuuint64_t strides[2] = {(cuuint64_t)pr.dn * 2, (cuuint64_t)pr.dn * d_k * 2};
+        const cuuint64_t dims[3] = {cols, (cuuint64_t)d_k, (cuuint64_t)pr.H};
+        const cuuint64_t strides[2] = {cols * 2, cols * d_k * 2};
         const cuuint32_t box[3] = {kChunk, 128, 1};
         if (encode_tiled(&km, bf16, 3, const_cast<void *>(w_uk), dims, strides, box, swz) != CUDA_SUCCESS)
             return KVATTN_ERR_UNSUPPORTED;
     }
     {
-        const cuuint64_t dims[3] = {(cuuint64_t)d_v, (cuuint64_t)pr.dn, (cuuint64_t)pr.H};
-        const cuuint64_t strides[2] = {(cuuint64_t)d_v * 2, (cuuint64_t)pr.dn * d_v * 2};
+        const cuuint64_t dims[3] = {(cuuint64_t)d_v, cols, (cuuint64_t)pr.H};
+        const cuuint64_t strides[2] = {(cuuint64_t)d_v * 2, cols * d_v * 2};
         const cuuint32_t box[3] = {64, kChunk, 1};
         if (encode_tiled(&vm, bf16, 3, const_cast<void *>(w_uv), dims, strides, box, swz) != CUDA_SUCCESS)
             return KVATTN_ERR_UNSUPPORTED;
     }
     for (int i = 0; i < 2; ++i) {
         const cuuint64_t width = (cuuint64_t)(i ? d_v : d_k);
-        const cuuint64_t dims[3] = {width, (cuuint64_t)max_kv_tokens, (cuuint64_t)pr.H};
+        const cuuint64_t dims[3] = {width, (cuuint64_t)max_kv_tokens, blocks};
         const cuuint64_t strides[2] = {width * 2, (cuuint64_t)max_kv_tokens * width * 2};
         const cuuint32_t box[3] = {64, 32, 1};
         if (encode_tiled(i ? &vo : &ko, bf16, 3, i ? v : k_nope, dims, strides, box, swz) != CUDA_SUCCESS)
@@ -586,6 +592,7 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.heads = pr.H;
     a.heads_per_group = pr.HPU;
     a.groups = pr.NU;
+    a.branches = pr.mlra ? pr.NU : 1;
     a.pairs_per_group = pairs;
     a.d_c = pr.dn;
     a.d_k = d_k;

@@ -88,7 +88,7 @@ struct PrefillArgs {
     void *out;
     float *lse;                                   // may be null
     int32_t *err;                                 // may be null
-    int heads, heads_per_kv;
+    int heads, heads_per_kv, heads_per_q;         // heads that share a key head, and a q_nope head
     int d_v, out_fp32, causal;
     int wide;                                     // output rows start on 32 bytes
     long long out_token_stride, out_head_stride;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int b = 0; b < NKB; ++b) {
                         unsigned char *dst = smem + (i * NKB + b) * kQBox;
                         if (b < NKN)
-                            tma_load_3d(dst, &m.q, 64 * b, it.head, row, &B.q_full[i]);
+                            tma_load_3d(dst, &m.q, 64 * b, it.head / a.heads_per_q, row, &B.q_full[i]);
                         else
                             tma_load_3d(dst, &m.qr, 0, it.head, row, &B.q_full[i]);
                     }
@@ -762,7 +762,8 @@ int validate_prefill(const kvattn_prefill_params *p)
 {
     if (!p || p->batch < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->d_nope < 1 || p->d_rope < 0 ||
         p->d_v < 1 || p->max_q_tokens < 0 || p->max_kv_tokens < 0 || (p->causal != 0 && p->causal != 1) ||
-        p->num_q_heads % p->num_kv_heads)
+        p->num_q_heads % p->num_kv_heads || p->num_q_nope_heads < 0 ||
+        (p->num_q_nope_heads > 0 && p->num_q_heads % p->num_q_nope_heads))
         return KVATTN_ERR_INVALID_ARG;
     if (p->out_dtype != KVATTN_OUT_BF16 && p->out_dtype != KVATTN_OUT_FP32)
         return KVATTN_ERR_INVALID_ARG;
@@ -812,11 +813,12 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
         return KVATTN_ERR_MISALIGNED;
     if (workspace_bytes < need)
         return KVATTN_ERR_WORKSPACE_TOO_SMALL;
-    const long long H = p->num_q_heads, KH = p->num_kv_heads, tq = p->max_q_tokens, tk = p->max_kv_tokens;
+    const long long H = p->num_q_heads, KH = p->num_kv_heads, QH = p->num_q_nope_heads ? p->num_q_nope_heads : H;
+    const long long tq = p->max_q_tokens, tk = p->max_kv_tokens;
     long long sq[2], sqr[2] = {8, 8}, sk[2], sv[2], so[2];
     const int64_t kr_given[2] = {p->k_rope_stride, 8};
     long long skr[2] = {8, 8};
-    if (!strides(p->q_nope_stride, H * p->d_nope, p->d_nope, sq) ||
+    if (!strides(p->q_nope_stride, QH * p->d_nope, p->d_nope, sq) ||
         !strides(p->k_stride, p->d_nope, (keys ? tk : 1) * p->d_nope, sk) ||
         !strides(p->v_stride, p->d_v, (keys ? tk : 1) * p->d_v, sv) || !strides(p->out_stride, H * p->d_v, p->d_v, so) ||
         (p->d_rope > 0 && (!strides(p->q_rope_stride, H * p->d_rope, p->d_rope, sqr) || !strides(kr_given, p->d_rope, 8, skr))))
@@ -830,7 +832,7 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     const long long rows = keys ? tk : 1;
     if (!keys)
         k_nope = v = k_rope = q_nope;
-    bool fine = rows_map(&m.q, q_nope, p->d_nope, (int)H, tq, sq, kTile) && rows_map(&m.k, k_nope, p->d_nope, (int)KH, rows, sk, kKeys) &&
+    bool fine = rows_map(&m.q, q_nope, p->d_nope, (int)QH, tq, sq, kTile) && rows_map(&m.k, k_nope, p->d_nope, (int)KH, rows, sk, kKeys) &&
                 rows_map(&m.v, v, p->d_v, (int)KH, rows, sv, kKeys);
     if (fine && p->d_rope > 0) {
         fine = rows_map(&m.qr, q_rope, p->d_rope, (int)H, tq, sqr, kTile);
@@ -870,6 +872,7 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     a.err = device_error;
     a.heads = (int)H;
     a.heads_per_kv = (int)(H / KH);
+    a.heads_per_q = (int)(H / QH);
     a.d_v = p->d_v;
     a.out_fp32 = p->out_dtype == KVATTN_OUT_FP32;
     a.causal = p->causal;

@@ -65,7 +65,7 @@ class kvattn_plan(ctypes.Structure):
 class kvattn_prefill_params(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "num_q_heads", "num_kv_heads", "d_nope", "d_rope", "d_v", "max_q_tokens", "max_kv_tokens",
-        "causal", "out_dtype")] + [(n, ctypes.c_int64 * 2) for n in (
+        "causal", "out_dtype", "num_q_nope_heads")] + [(n, ctypes.c_int64 * 2) for n in (
             "q_nope_stride", "q_rope_stride", "k_stride", "v_stride", "out_stride")] + [
         ("k_rope_stride", ctypes.c_int64)]
 
@@ -431,9 +431,9 @@ def append_slots_tensor(variant, params, new_kv, pos, slots, kv_cache, rope_base
 def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_uv, max_kv_tokens,
                       device_error=None) -> dict:
     """``kvattn_expand_kv`` on tensors: w_uk [H][d_k][d_nope], w_uv
-    [H][d_nope][d_v].  Returns k [H][max_kv_tokens][d_k], v
-    [H][max_kv_tokens][d_v] and k_rope [max_kv_tokens][d_rope] (None without a
-    rope part)."""
+    [H][d_nope][d_v] (MLRA: R * d_nope).  Returns k [H][max_kv_tokens][d_k], v
+    [H][max_kv_tokens][d_v] (MLRA: H * R blocks) and k_rope
+    [max_kv_tokens][d_rope] (None without a rope part)."""
     import torch
     dev, bf16, at = kv_cache.get_device(), torch.bfloat16, kv_cache.device
     H, dn, dr, B, n = params.num_q_heads, params.d_nope, params.d_rope, params.batch, int(max_kv_tokens)
@@ -442,13 +442,14 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
         raise ValueError("kv_cache is not the pool that params describe")
     h1, d_k, c1 = _dense(w_uk, bf16, 3, dev, "w_uk").shape
     h2, c2, d_v = _dense(w_uv, bf16, 3, dev, "w_uv").shape
-    if h1 != H or h2 != H or c1 != dn or c2 != dn or _dense(kv_start, torch.int32, 1, dev, "kv_start").numel() != B + 1:
-        raise ValueError("w_uk is [H][d_k][d_nope], w_uv [H][d_nope][d_v], kv_start [batch + 1]")
+    R = params.num_kv if int(variant) == KVATTN_MLRA else 1
+    if h1 != H or h2 != H or c1 != R * dn or c2 != R * dn or _dense(kv_start, torch.int32, 1, dev, "kv_start").numel() != B + 1:
+        raise ValueError("w_uk is [H][d_k][d_nope], w_uv [H][d_nope][d_v] (MLRA: R * d_nope), kv_start [batch + 1]")
     if block_table is not None and _dense(block_table, torch.int32, 2, dev, "block_table").shape != (
             B, params.max_pages_per_seq):
         raise ValueError("block_table is [batch][max_pages_per_seq]")
-    k = torch.empty((H, n, d_k), dtype=bf16, device=at)
-    v = torch.empty((H, n, d_v), dtype=bf16, device=at)
+    k = torch.empty((H * R, n, d_k), dtype=bf16, device=at)
+    v = torch.empty((H * R, n, d_v), dtype=bf16, device=at)
     k_rope = torch.empty((n, dr), dtype=bf16, device=at) if dr else None
     if n:
         ws = torch.empty(kvattn_expand_workspace_size(variant, params, n), dtype=torch.uint8, device=at)
@@ -461,8 +462,8 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
 
 def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, causal=True, out=None, lse=None,
                     out_fp32=False, device_error=None) -> dict:
-    """``kvattn_prefill`` on bf16 tensors: q_nope [T][H][d_nope], q_rope
-    [T][H][d_rope] or None, k [KH][Tk][d_nope], v [KH][Tk][d_v], k_rope
+    """``kvattn_prefill`` on bf16 tensors: q_nope [T][H][d_nope] (or fewer
+    heads, that divide H), q_rope [T][H][d_rope] or None, k [KH][Tk][d_nope], v [KH][Tk][d_v], k_rope
     [Tk][d_rope] or None, in any strides with a contiguous last axis (keys laid
     out token by token: ``k.transpose(0, 1)``); q_start and kv_start int32
     [B + 1].  Returns out [T][H][d_v] and lse [T][H]; rows past the last
@@ -476,14 +477,15 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
     ks = _last_axis(k, bf16, 3, dev, "k")
     vs = _last_axis(v, bf16, 3, dev, "v")
     (T, H, dn), (KH, Tk, d_v) = q_nope.shape, v.shape
+    QH = H
     B = _dense(q_start, torch.int32, 1, dev, "q_start").numel() - 1
     if k.shape != (KH, Tk, dn) or _dense(kv_start, torch.int32, 1, dev, "kv_start").numel() != B + 1:
         raise ValueError("the shapes of queries, keys, values and starts do not fit together")
     dr, rs, krs = 0, (0, 0), 0
     if rope:
         rs, krs = _last_axis(q_rope, bf16, 3, dev, "q_rope"), _last_axis(k_rope, bf16, 2, dev, "k_rope")[0]
-        dr = q_rope.shape[2]
-        if q_rope.shape != (T, H, dr) or k_rope.shape != (Tk, dr):
+        t2, H, dr = q_rope.shape
+        if t2 != T or k_rope.shape != (Tk, dr):
             raise ValueError("the shapes of queries, keys, values and starts do not fit together")
     dtype = torch.float32 if out_fp32 else bf16
     if out is None:
@@ -498,9 +500,9 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
         raise ValueError("lse is [T][H]")
     if T:
         # an axis of one element has no stride of its own
-        t1, h1, k1, kh1 = T > 1, H > 1, Tk > 1, KH > 1
+        t1, h1, qh1, k1, kh1 = T > 1, H > 1, QH > 1, Tk > 1, KH > 1
         p = kvattn_prefill_params(B, H, KH, dn, dr, d_v, T, Tk, 1 if causal else 0,
-                                  KVATTN_OUT_FP32 if out_fp32 else KVATTN_OUT_BF16, (qs[0] * t1, qs[1] * h1),
+                                  KVATTN_OUT_FP32 if out_fp32 else KVATTN_OUT_BF16, QH, (qs[0] * t1, qs[1] * qh1),
                                   (rs[0] * t1, rs[1] * h1), (ks[1] * k1, ks[0] * kh1), (vs[1] * k1, vs[0] * kh1),
                                   (os[0] * t1, os[1] * h1), krs * k1)
         ws = torch.empty(kvattn_prefill_workspace_size(p), dtype=torch.uint8, device=at)

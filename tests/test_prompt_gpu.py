@@ -342,6 +342,22 @@ def test_expand_matches_reference(dev, H, G, dc, dr, dk, dv, lens, paged):
     check_expand(got, cache, table, uk, uv, G, lens, mpps)
 
 
+@pytest.mark.parametrize("H,R,dc,dk,dv", [(6, 4, 128, 128, 128), (3, 2, 64, 64, 40)])
+def test_expand_branches(dev, H, R, dc, dk, dv):
+    """MLRA: every head's keys and values of each branch, weights' blocks side by side and stacked."""
+    rng = np.random.default_rng(R)
+    lens = [130, 0, 65]
+    cache, table, _, _, p, mpps = expand_case(rng, dev, H, R, dc, 32, dk, dv, lens)
+    uk, uv = bits(rng, H, dk, R * dc, scale=dc ** -0.5), bits(rng, H, R * dc, dv, scale=dc ** -0.5)
+    got = K.expand_kv_tensors(K.KVATTN_MLRA, p, up(cache, dev), i32(table, dev), i32(starts(lens), dev), up(uk, dev), up(uv, dev),
+                              sum(lens))
+    assert got["k"].shape == (H * R, sum(lens), dk)
+    for r in range(R):
+        cols = np.r_[r * dc:(r + 1) * dc, R * dc:R * dc + 32]
+        one = dict(k=got["k"][r::R], v=got["v"][r::R], k_rope=got["k_rope"])
+        check_expand(one, cache[..., cols], table, uk[..., r * dc:(r + 1) * dc], uv[:, r * dc:(r + 1) * dc], 1, lens, mpps)
+
+
 def test_expand_leaves_rows_past_the_last_sequence(dev):
     import torch
     rng = np.random.default_rng(2)
@@ -443,6 +459,17 @@ def test_prefill_head_layouts(dev, H, KH, dn, dr, dv, fp32):
     x = prefill_case(rng, H, KH, dn, dr, dv, ql, kl)
     got = call(dev, x, ql, kl, (dn + dr) ** -0.5, True, out_fp32=fp32)
     check_prefill(got, x, ql, kl, (dn + dr) ** -0.5, True, fp32)
+
+
+def test_prefill_heads_that_share_q_nope(dev):
+    rng = np.random.default_rng(22)
+    ql, kl = [140, 20], [140, 300]
+    x = prefill_case(rng, 12, 12, 128, 64, 128, ql, kl)
+    q = x["q"][:, :3].copy()
+    x["q"] = np.repeat(q, 4, axis=1)
+    t = {k: up(v, dev) for k, v in x.items()}
+    got = K.prefill_tensors(up(q, dev), t["qr"], t["k"], t["kr"], t["v"], i32(starts(ql), dev), i32(starts(kl), dev), 0.08)
+    check_prefill(got, x, ql, kl, 0.08, True)
 
 
 @pytest.mark.parametrize("scale", [-0.07, 0.0, 1.0])
@@ -594,7 +621,7 @@ def test_prefill_twice_is_the_same_and_streams_do_not_meet(dev):
 
 # ------------------------------------------------------------- all together
 
-@pytest.mark.parametrize("name", ["mla", "gla"])
+@pytest.mark.parametrize("name", ["mla", "gla", "mlra_128k"])
 def test_a_prompt_then_tokens(dev, name):
     """Tables, append, expand and prefill of two chunks, then the last token of
     every sequence through the absorbed decode on the same cache: the expanded
@@ -608,9 +635,10 @@ def test_a_prompt_then_tokens(dev, name):
     B, mpps, pages = 3, 12, 40
     chunks = [[300, 1, 129], [64, 200, 0]]
     row = G * dc + dr
-    variant = K.VARIANTS[name]
+    variant = s.variant_id
+    R = G if s.variant == "mlra" else 1            # branches: the output is the sum over them
     cache = torch.full((pages, 64, row), float("nan"), dtype=torch.bfloat16, device=dev)
-    uk, uv = bits(rng, H, dh, dc, scale=dc ** -0.5), bits(rng, H, dc, dh, scale=dh ** -0.5)
+    uk, uv = bits(rng, H, dh, R * dc, scale=dc ** -0.5), bits(rng, H, R * dc, dh, scale=dh ** -0.5)
     tuk, tuv = up(uk, dev), up(uv, dev)
     lens, table, count = i32([0] * B, dev), i32(np.full((B, mpps), -1), dev), i32([pages], dev)
     pool = i32(rng.permutation(pages), dev)
@@ -619,16 +647,17 @@ def test_a_prompt_then_tokens(dev, name):
     err = word(dev)
     for new in chunks:
         T = sum(new)
-        rows, q, qr = bits(rng, T, row), bits(rng, T, H, dh), bits(rng, T, H, dr)
+        rows, q, qr = bits(rng, T, row), bits(rng, T, H, dh), bits(rng, T, H * R, dr)
         tq, tqr = up(q, dev), up(qr, dev)
         st = K.build_tables_tensors(lens, i32(new, dev), pool, count, table, T + 10, err, inplace=True)
         p = K.make_params(B, H, G, dc, dr, mpps, pages, 0)
         K.append_slots_tensor(variant, p, up(rows, dev), st["pos"][:T].contiguous(), st["slots"][:T].contiguous(), cache,
                               W.ROPE_BASE, err)
-        K.rope_tensor(tqr, st["pos"], 0, dr, W.ROPE_BASE, H)
+        K.rope_tensor(tqr, st["pos"], 0, dr, W.ROPE_BASE, H * R)
         total = int(st["kv_start"][-1])
         e = K.expand_kv_tensors(variant, p, cache, table, st["kv_start"], tuk, tuv, total, err)
         got = K.prefill_tensors(tq, tqr, e["k"], e["k_rope"], e["v"], st["q_start"], st["kv_start"], scale, device_error=err)
+        total_out = got["out"].view(T, H, R, dh).double().sum(2)
         # the fp64 chain
         at, off, num, den = 0, 0.0, 0.0, 0.0
         from oracle import steps
@@ -638,26 +667,30 @@ def test_a_prompt_then_tokens(dev, name):
             if n:
                 r[:, G * dc:] = steps.rope(r[:, G * dc:], pos, W.ROPE_BASE)
             past[b] = np.concatenate([past[b], r])
-            k, v, _, _ = prompt.expand(past[b], f64(uk), f64(uv), G)
-            for h in range(H if n else 0):
-                qq = np.concatenate([f64(q[at:at + n, h]), steps.rope(f64(qr[at:at + n, h]), pos, W.ROPE_BASE)], 1)
-                ref = prompt.attention(qq, np.concatenate([k[h], past[b][:, G * dc:]], 1), v[h], scale, True)[0]
-                num += ((down(got["out"][at:at + n, h]) - ref) ** 2).sum()
-                den += (ref ** 2).sum()
+            ref = np.zeros((H, n, dh))
+            for r in range(R):
+                cols = slice(r * dc, (r + 1) * dc) if R > 1 else slice(0, G * dc)
+                wc = cols if R > 1 else slice(None)
+                k, v, _, _ = prompt.expand(past[b][:, cols], f64(uk)[:, :, wc], f64(uv)[:, wc], 1 if R > 1 else G)
+                for h in range(H if n else 0):
+                    qq = np.concatenate([f64(q[at:at + n, h]), steps.rope(f64(qr[at:at + n, h * R + r]), pos, W.ROPE_BASE)], 1)
+                    ref[h] += prompt.attention(qq, np.concatenate([k[h], past[b][:, G * dc:]], 1), v[h], scale, True)[0]
+            num += ((down(total_out[at:at + n]).transpose(1, 0, 2) - ref) ** 2).sum()
+            den += (ref ** 2).sum()
             at += n
         assert np.sqrt(num / den) <= 1e-2
     assert int(err.item()) == 0
     # the newest token of each sequence again, absorbed
     last = [0, chunks[1][0] + chunks[1][1] - 1]
     idx = torch.tensor([chunks[1][0] - 1, chunks[1][0] + chunks[1][1] - 1], device=dev)
-    p = K.make_params(2, H, G, dc, dr, mpps, pages, 500)
+    p = K.make_params(2, H, G, dc, dr, mpps, pages, 500, branch_out=1 if R > 1 else 0)
     qa = K.head_proj_tensor(tq[idx].contiguous(), tuk)
-    ol = torch.empty(2, H, dc, dtype=torch.bfloat16, device=dev)
-    lse = torch.empty(2, H, dtype=torch.float32, device=dev)
+    ol = torch.empty(2, H, R * dc, dtype=torch.bfloat16, device=dev)
+    lse = torch.empty(2, H * R, dtype=torch.float32, device=dev)
     ws = torch.zeros(K.kvattn_workspace_size(variant, p), dtype=torch.uint8, device=dev)
     K.decode_tensors(variant, p, qa, tqr[idx].contiguous(), cache, table, lens, scale, ol, lse, ws)
     one = down(K.head_proj_tensor(ol, tuv))
-    two = down(got["out"][idx])
+    two = down(total_out[idx])
     assert len(last) == 2 and np.linalg.norm(one - two) <= 1.5e-2 * np.linalg.norm(two)
     # lse of the two forms: keys rounded to bf16 in one, the absorbed query in the other
     assert np.abs(down(lse) - down(got["lse"][idx])).max() <= 2e-2

@@ -78,7 +78,7 @@ def expand(variant=K.KVATTN_MLA, n=500, d_k=128, d_v=128, ws_bytes=1 << 30, err=
 @pytest.mark.parametrize("kw,status", [
     (dict(n=-1), INVALID), (dict(d_k=0), INVALID), (dict(d_k=132), UNSUPPORTED), (dict(d_k=136), UNSUPPORTED),
     (dict(d_v=60), UNSUPPORTED), (dict(d_nope=72), UNSUPPORTED), (dict(ws_bytes=100), SMALL),
-    (dict(variant=K.KVATTN_MLRA), UNSUPPORTED), (dict(variant=K.KVATTN_GQA, d_rope=0), UNSUPPORTED),
+    (dict(variant=K.KVATTN_GTA, d_rope=0), UNSUPPORTED), (dict(variant=K.KVATTN_GQA, d_rope=0), UNSUPPORTED),
     (dict(ptr=dict(ws=FAKE + 16)), MISALIGNED), (dict(err=FAKE + 2), MISALIGNED), (dict(n=0), 0),
     (dict(batch=16385), UNSUPPORTED), (dict(page_size=32), UNSUPPORTED), (dict(n=2 ** 31 - 2), UNSUPPORTED),
 ])
@@ -95,7 +95,7 @@ def test_expand_null_and_misaligned_pointers(lib, name):
 # ----------------------------------------------------------------- prefill
 def params(**kw):
     d = dict(batch=2, num_q_heads=8, num_kv_heads=4, d_nope=128, d_rope=64, d_v=128, max_q_tokens=500, max_kv_tokens=700,
-             causal=1, out_dtype=0)
+             causal=1, out_dtype=0, num_q_nope_heads=0)
     d.update({k: v for k, v in kw.items() if not k.endswith("stride")})
     p = K.kvattn_prefill_params(*d.values())
     for k, v in kw.items():
@@ -118,7 +118,7 @@ def prefill(scale=0.1, lse=FAKE, err=None, ws_bytes=1 << 30, ptr=None, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=0), INVALID), (dict(num_q_heads=0), INVALID), (dict(num_kv_heads=3), INVALID), (dict(d_nope=0), INVALID),
     (dict(d_rope=-8), INVALID), (dict(d_v=0), INVALID), (dict(causal=2), INVALID), (dict(out_dtype=5), INVALID),
-    (dict(max_q_tokens=-1), INVALID), (dict(max_kv_tokens=-1), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(num_q_nope_heads=3), INVALID), (dict(num_q_nope_heads=-1), INVALID), (dict(max_q_tokens=-1), INVALID), (dict(max_kv_tokens=-1), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(d_nope=100), UNSUPPORTED), (dict(d_nope=256), UNSUPPORTED), (dict(d_rope=72), UNSUPPORTED), (dict(d_v=136), UNSUPPORTED),
     (dict(batch=16385), UNSUPPORTED), (dict(max_q_tokens=2 ** 31 - 1, num_q_heads=65535, num_kv_heads=1), UNSUPPORTED),
     (dict(ws_bytes=255), SMALL), (dict(lse=FAKE + 2), MISALIGNED), (dict(err=FAKE + 2), MISALIGNED),
@@ -141,7 +141,7 @@ def test_workspace_sizes_cover_a_tile_for_every_sequence(lib):
     p = K.make_params(5, 16, 1, 512, 64, 4, 9, 0)
     assert K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, 129) >= 32 * (2 + 5)
     with pytest.raises(K.KvattnError):
-        K.kvattn_expand_workspace_size(K.KVATTN_MLRA, p, 129)
+        K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, -1)
 
 
 def test_helpers_check_shapes_and_types(lib):
