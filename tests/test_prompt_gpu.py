@@ -424,7 +424,7 @@ def check_prefill(got, x, ql, kl, scale, causal, fp32=False, skip=()):
             assert np.all(np.abs(out[a:e, h] - ro) <= tol), (b, h, np.abs(out[a:e, h] - ro).max())
             none = np.isinf(rl)
             np.testing.assert_array_equal(lse[a:e, h][none], rl[none])
-            assert np.all(np.abs(lse[a:e, h] - rl)[~none] <= (delta + 2.0 ** -22 * np.abs(rl))[~none]), (b, h)
+            assert np.all(np.abs(lse[a:e, h][~none] - rl[~none]) <= delta[~none] + 2.0 ** -22 * np.abs(rl[~none])), (b, h)
 
 
 def call(dev, x, ql, kl, scale, causal, **kw):
@@ -617,6 +617,67 @@ def test_prefill_twice_is_the_same_and_streams_do_not_meet(dev):
     torch.cuda.synchronize()
     for y in got + [kept]:
         assert torch.equal(one, y)
+
+
+def test_prefill_and_expand_of_the_largest_batch(dev):
+    """16384 sequences of no or one token."""
+    rng = np.random.default_rng(23)
+    ql = rng.integers(0, 2, 16384).tolist()
+    x = prefill_case(rng, 1, 1, 8, 0, 8, ql, ql)
+    err = word(dev)
+    got = call(dev, x, ql, ql, 0.1, True, device_error=err)
+    assert int(err.item()) == 0
+    n = sum(ql)
+    # one key each: the output is its value, lse the score
+    np.testing.assert_array_equal(down(got["out"])[:n, 0], f64(x["v"][0, :n]))
+    s = 0.1 * (f64(x["q"][:n, 0]) * f64(x["k"][0, :n])).sum(1)
+    assert np.abs(down(got["lse"])[:n, 0] - s).max() <= 1e-5
+    cache, table, uk, uv, p, mpps = expand_case(rng, dev, 2, 1, 64, 8, 8, 8, ql)
+    e = K.expand_kv_tensors(K.KVATTN_MLA, p, up(cache, dev), i32(table, dev), i32(starts(ql), dev), up(uk, dev), up(uv, dev), n, err)
+    assert int(err.item()) == 0
+    rows = np.array([f64(cache[table[b, 0], 0]) for b in range(16384) if ql[b]])
+    k, v, ka, va = prompt.expand(rows, f64(uk), f64(uv), 1)
+    assert np.all(np.abs(down(e["k"]) - k) <= BF16 * np.abs(k) + 1e-5 * ka)
+    assert np.all(np.abs(down(e["v"]) - v) <= BF16 * np.abs(v) + 1e-5 * va)
+
+
+def test_offsets_past_32_bits_in_the_cache(dev):
+    """A pool of more than 2^31 elements: rows appended to and expanded from its last pages."""
+    import torch
+    rng = np.random.default_rng(24)
+    row, pages, n = 576, 60000, 100
+    assert (pages - 3) * 64 * row > 2 ** 31
+    cache = torch.empty(pages, 64, row, dtype=torch.bfloat16, device=dev)
+    cache[-3:] = 0
+    rows, table = bits(rng, n, row), np.array([[pages - 1, pages - 3]])
+    slots = np.concatenate([(pages - 1) * 64 + np.arange(64), (pages - 3) * 64 + np.arange(n - 64)])
+    p = K.make_params(1, 4, 1, 512, 64, 2, pages, 0)
+    K.append_slots_tensor(K.KVATTN_MLA, p, up(rows, dev), None, i32(slots, dev), cache, 0.0)
+    np.testing.assert_array_equal(down(cache[-1]), f64(rows[:64]))
+    np.testing.assert_array_equal(down(cache[-3, :n - 64]), f64(rows[64:]))
+    uk, uv = bits(rng, 4, 128, 512, scale=512 ** -0.5), bits(rng, 4, 512, 128, scale=512 ** -0.5)
+    e = K.expand_kv_tensors(K.KVATTN_MLA, p, cache, i32(table, dev), i32([0, n], dev), up(uk, dev), up(uv, dev), n)
+    k, v, ka, va = prompt.expand(f64(rows), f64(uk), f64(uv), 1)
+    assert np.all(np.abs(down(e["k"]) - k) <= BF16 * np.abs(k) + 1e-5 * ka)
+    assert np.all(np.abs(down(e["v"]) - v) <= BF16 * np.abs(v) + 1e-5 * va)
+
+
+def test_offsets_past_32_bits_in_the_rows(dev):
+    """Queries, keys, values and outputs of more than 2^31 elements; the sequence stands at their end."""
+    import torch
+    rng = np.random.default_rng(25)
+    T, nq, nk = 8_500_000, 140, 300
+    assert (T - nk) * 256 > 2 ** 31
+    x = prefill_case(rng, 2, 2, 128, 0, 128, [nq], [nk], slack=0)
+
+    def far(t, axis, shape):
+        big = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        big.narrow(axis, T - t.shape[axis], t.shape[axis]).copy_(t)
+        return big
+    q = far(up(x["q"], dev), 0, (T, 2, 128))
+    k, v = far(up(x["k"], dev), 1, (2, T, 128)), far(up(x["v"], dev), 1, (2, T, 128))
+    got = K.prefill_tensors(q, None, k, None, v, i32([T - nq, T], dev), i32([T - nk, T], dev), 0.1)
+    check_prefill(dict(out=got["out"][T - nq:], lse=got["lse"][T - nq:]), x, [nq], [nk], 0.1, True)
 
 
 # ------------------------------------------------------------- all together
