@@ -354,12 +354,13 @@ def _last_axis(t, dtype, dims, index, what):
 def _enqueue(what, index, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, with that device
     current (a kernel runs on the device that is current at its launch)."""
-    from torch import _C, cuda
-    if cuda.current_device() == index:
-        st = fn(*args, _C._cuda_getCurrentRawStream(index))
+    import torch
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, stream)
     else:
-        with cuda.device(index):
-            st = fn(*args, _C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
     if st:
         raise KvattnError(st, what)
 
@@ -389,7 +390,7 @@ def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_ta
         raise ValueError("cached_lens, new_lens and block_table have one row a request, free_count one value")
     # the outputs share one allocation, pos and slots in front (on 16 bytes)
     sizes = [n, n, B + 1, B + 1] if inplace else [n, n, B + 1, B + 1, B, 1]
-    r = torch.empty(sum(sizes), dtype=i32, device=cached_lens.device)
+    r = cached_lens.new_empty(sum(sizes))
     pos = r.data_ptr()
     slots, q_start, kv_start, end = pos + 4 * n, pos + 8 * n, pos + 8 * n + 4 * B + 4, pos + 8 * n + 8 * B + 8
     if inplace:
@@ -399,7 +400,7 @@ def build_tables_tensors(cached_lens, new_lens, free_pages, free_count, block_ta
     _enqueue("kvattn_build_tables", dev, load().kvattn_build_tables, B, mpps, free_pages.shape[0], n,
              cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
              block_table.data_ptr(), lens, left, q_start, kv_start, pos, slots, _error_word(device_error, dev))
-    v = r.split(sizes)
+    v = torch.split_with_sizes(r, sizes)
     return dict(block_table=block_table, pos=v[0], slots=v[1], q_start=v[2], kv_start=v[3],
                 seq_lens=cached_lens if inplace else v[4], free_left=free_count if inplace else v[5])
 
@@ -435,7 +436,7 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
     [H][max_kv_tokens][d_v] (MLRA: H * R blocks) and k_rope
     [max_kv_tokens][d_rope] (None without a rope part)."""
     import torch
-    dev, bf16, at = kv_cache.get_device(), torch.bfloat16, kv_cache.device
+    dev, bf16 = kv_cache.get_device(), torch.bfloat16
     H, dn, dr, B, n = params.num_q_heads, params.d_nope, params.d_rope, params.batch, int(max_kv_tokens)
     if _dense(kv_cache, bf16, kv_cache.dim(), dev, "kv_cache").numel() != params.num_pages * 64 * (
             params.num_kv * dn + dr):
@@ -448,14 +449,14 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
     if block_table is not None and _dense(block_table, torch.int32, 2, dev, "block_table").shape != (
             B, params.max_pages_per_seq):
         raise ValueError("block_table is [batch][max_pages_per_seq]")
-    k = torch.empty((H * R, n, d_k), dtype=bf16, device=at)
-    v = torch.empty((H * R, n, d_v), dtype=bf16, device=at)
-    k_rope = torch.empty((n, dr), dtype=bf16, device=at) if dr else None
+    k, v = kv_cache.new_empty((H * R, n, d_k)), kv_cache.new_empty((H * R, n, d_v))
+    k_rope = kv_cache.new_empty((n, dr)) if dr else None
     if n:
-        ws = torch.empty(kvattn_expand_workspace_size(variant, params, n), dtype=torch.uint8, device=at)
+        ws_bytes = kvattn_expand_workspace_size(variant, params, n)
+        ws = kv_cache.new_empty(ws_bytes // 2)
         _enqueue("kvattn_expand_kv", dev, load().kvattn_expand_kv, int(variant), ctypes.byref(params),
                  kv_cache.data_ptr(), _ptr(block_table), kv_start.data_ptr(), n, d_k, d_v, w_uk.data_ptr(),
-                 w_uv.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_rope), ws.data_ptr(), ws.numel(),
+                 w_uv.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_rope), ws.data_ptr(), ws_bytes,
                  _error_word(device_error, dev))
     return dict(k=k, v=v, k_rope=k_rope)
 
@@ -469,7 +470,7 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
     [B + 1].  Returns out [T][H][d_v] and lse [T][H]; rows past the last
     sequence are left as they were."""
     import torch
-    dev, bf16, at = q_nope.get_device(), torch.bfloat16, q_nope.device
+    dev, bf16 = q_nope.get_device(), torch.bfloat16
     rope = q_rope is not None
     if rope != (k_rope is not None):
         raise ValueError("q_rope and k_rope go together")
@@ -489,13 +490,13 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
             raise ValueError("the shapes of queries, keys, values and starts do not fit together")
     dtype = torch.float32 if out_fp32 else bf16
     if out is None:
-        out, os = torch.empty((T, H, d_v), dtype=dtype, device=at), (0, 0)
+        out, os = q_nope.new_empty((T, H, d_v), dtype=dtype), (0, 0)
     else:
         os = _last_axis(out, dtype, 3, dev, "out")
         if out.shape != (T, H, d_v):
             raise ValueError("out is [T][H][d_v]")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=at)
+        lse = q_nope.new_empty((T, H), dtype=torch.float32)
     elif _dense(lse, torch.float32, 2, dev, "lse").shape != (T, H):
         raise ValueError("lse is [T][H]")
     if T:
@@ -505,8 +506,9 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
                                   KVATTN_OUT_FP32 if out_fp32 else KVATTN_OUT_BF16, QH, (qs[0] * t1, qs[1] * qh1),
                                   (rs[0] * t1, rs[1] * h1), (ks[1] * k1, ks[0] * kh1), (vs[1] * k1, vs[0] * kh1),
                                   (os[0] * t1, os[1] * h1), krs * k1)
-        ws = torch.empty(kvattn_prefill_workspace_size(p), dtype=torch.uint8, device=at)
+        ws_bytes = kvattn_prefill_workspace_size(p)
+        ws = q_nope.new_empty(ws_bytes // 2)
         _enqueue("kvattn_prefill", dev, load().kvattn_prefill, ctypes.byref(p), q_nope.data_ptr(), _ptr(q_rope),
                  k.data_ptr(), _ptr(k_rope), v.data_ptr(), q_start.data_ptr(), kv_start.data_ptr(), sm_scale,
-                 out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _error_word(device_error, dev))
+                 out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws_bytes, _error_word(device_error, dev))
     return dict(out=out, lse=lse)
