@@ -52,6 +52,8 @@ struct Bars {
     uint64_t d_full[2], d_empty[2];
     uint64_t done;
     uint32_t tmem_base;
+    int32_t ntiles;
+    ragged::Tile tiles[ragged::kSmallTiles];
 };
 
 constexpr int stages_of(int chunks)
@@ -111,8 +113,8 @@ __device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *map, 
 }
 
 struct ExpandArgs {
-    const int32_t *header;
-    const ragged::Tile *tiles;
+    ragged::PlanArgs plan;
+    int listed;                                 // the plan kernel has listed the tiles; else every CTA does
     const int32_t *block_table;                 // nullptr: contiguous
     const __nv_bfloat16 *cache;
     __nv_bfloat16 *k, *v, *k_rope;
@@ -215,10 +217,10 @@ struct Walk {
 };
 
 // The tile of CTA `rank` in the walk's tile pair (no rows where the list ends).
-__device__ __forceinline__ ragged::Tile pair_tile(const ExpandArgs &a, const Walk &w, int ntiles, int rank)
+__device__ __forceinline__ ragged::Tile pair_tile(const ragged::Tile *tiles, const Walk &w, int ntiles, int rank)
 {
     const int i = 2 * w.tiles + rank;
-    ragged::Tile t = a.tiles[min(i, ntiles - 1)];
+    ragged::Tile t = tiles[min(i, ntiles - 1)];
     if (i >= ntiles)
         t.nq = 0;
     return t;
@@ -260,12 +262,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 0)
         tmem_alloc2(&B.tmem_base, 512);
+    if (warp == 1 && !a.listed) {
+        const int n = ragged::list_tiles(a.plan, B.tiles, blockIdx.x == 0);
+        if (lane == 0)
+            B.ntiles = n;
+    }
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tbase = B.tmem_base;
-    pdl_wait_primary();                          // the tile list
-    const int ntiles = a.header[0];
+    if (a.listed)
+        pdl_wait_primary();                      // the tile list
+    const int ntiles = a.listed ? a.plan.header[0] : B.ntiles;
+    const ragged::Tile *const tiles = a.listed ? a.plan.tiles : B.tiles;
     Walk w(a, ntiles);
     bool ok = true;
 
@@ -282,8 +291,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     }
                     ++na;
-                    const ragged::Tile t = pair_tile(a, w, ntiles, rank);
-                    const int subs = pages_in(t), both = subs + pages_in(pair_tile(a, w, ntiles, rank ^ 1));
+                    const ragged::Tile t = pair_tile(tiles, w, ntiles, rank);
+                    const int subs = pages_in(t), both = subs + pages_in(pair_tile(tiles, w, ntiles, rank ^ 1));
                     int y[2] = {0, 0};
                     for (int s = 0; s < subs; ++s)
                         y[s] = page_or_none(a, t.seq, t.tok0 / kPage + s, w.group == 0) * kPage;
@@ -381,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (; w.more(); w.next()) {
             if (w.group || w.pair || !vecs)
                 continue;
-            const ragged::Tile t = pair_tile(a, w, ntiles, rank);
+            const ragged::Tile t = pair_tile(tiles, w, ntiles, rank);
             for (int i = lane; i < t.nq * vecs; i += 32) {
                 const int r = i / vecs, p = i % vecs;
                 const int page = page_or_none(a, t.seq, (t.tok0 + r) / kPage, false);
@@ -403,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t policy = pass_policy();
         uint32_t nd = 0, no = 0;
         for (; ok && w.more(); w.next()) {
-            const ragged::Tile t = pair_tile(a, w, ntiles, rank);
+            const ragged::Tile t = pair_tile(tiles, w, ntiles, rank);
             const int q0 = t.q0, nq = t.nq;
             const bool whole = (warp & 3) * 32 + 32 <= nq;
             const int heads = min(2, a.heads_per_group - 2 * w.pair);
@@ -578,11 +587,12 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     pa.header = reinterpret_cast<int32_t *>(ws);
     pa.tiles = reinterpret_cast<ragged::Tile *>(ws + ragged::kPlanHeader);
     pa.err = device_error;
-    if (ragged::launch_plan(pa, s) != cudaSuccess)
+    const bool listed = !ragged::small_plan(pa.batch, cap);
+    if (listed && ragged::launch_plan(pa, s) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     ExpandArgs a{};
-    a.header = pa.header;
-    a.tiles = pa.tiles;
+    a.plan = pa;
+    a.listed = listed;
     a.block_table = block_table;
     a.cache = static_cast<const __nv_bfloat16 *>(kv_cache);
     a.k = static_cast<__nv_bfloat16 *>(k_nope);
@@ -616,7 +626,7 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = listed ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, expand_kernel, cm, km, vm, ko, vo, (const ExpandArgs)a) == cudaSuccess ? KVATTN_OK
                                                                                                    : KVATTN_ERR_CUDA;
 }

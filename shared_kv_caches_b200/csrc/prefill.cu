@@ -85,8 +85,8 @@ constexpr int kBarBytes = 1024;
 constexpr int kSmemMax = 227 * 1024;
 
 struct PrefillArgs {
-    int32_t *header;                              // [0] tiles, [1] items handed out (0 at the start)
-    const ragged::Tile *tiles;
+    ragged::PlanArgs plan;                        // header: [0] tiles, [1] items handed out (0 at the start)
+    int listed;                                   // the plan kernel has listed the tiles; else every CTA does
     void *out;
     float *lse;                                   // may be null
     int32_t *err;                                 // may be null
@@ -132,6 +132,7 @@ struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
+    ragged::Tile tiles[ragged::kSmallTiles];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], s_free[2];                // scores formed; scores in registers
     uint64_t p_full[2];                           // probabilities stored
@@ -214,12 +215,12 @@ __device__ __forceinline__ void store_row(void *p, const uint32_t *r, bool wide)
 }
 
 // Item i of the list: groups of kHeadGroup heads (the rest in one group), then tiles, then heads.
-__device__ __forceinline__ Item get_item(const PrefillArgs &a, int ntiles, int i)
+__device__ __forceinline__ Item get_item(const PrefillArgs &a, const ragged::Tile *tiles, int ntiles, int i)
 {
     const int per_group = ntiles * kHeadGroup;
     const int g = min(i / per_group, a.head_groups), r = i - g * per_group;
     const int hc = g < a.head_groups ? kHeadGroup : a.heads - g * kHeadGroup;
-    const ragged::Tile t = a.tiles[r / hc];
+    const ragged::Tile t = tiles[r / hc];
     Item it;
     it.q0 = t.q0;
     it.nq = t.nq;
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_regs_down<kIssueRegs>();
         if (warp == 0) {
             // ---------------------------------------------------------------- TMA
+            const int ntiles = a.listed ? a.plan.header[0] : ragged::list_tiles(a.plan, B.tiles, blockIdx.x == 0);
             if (lane == 0) {
                 uint32_t kn = 0, vn = 0;                     // key and value tiles loaded
                 uint32_t qn[2] = {0, 0};                     // query tiles loaded
@@ -364,11 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // items are handed out as CTAs get to them: the first by the block's
                 // number, then by a count that the plan kernel sets to 0
                 // (an item is looked up while the one before is loaded)
-                const int ntiles = a.header[0], items = ntiles * a.heads;
+                const ragged::Tile *const tiles = a.listed ? a.plan.tiles : B.tiles;
+                const int items = ntiles * a.heads;
                 auto look_up = [&](int i) -> Item {
                     Item it{};
                     it.head = -1;
-                    return i < items ? get_item(a, ntiles, i) : it;
+                    return i < items ? get_item(a, tiles, ntiles, i) : it;
                 };
                 Item next = look_up(blockIdx.x);
                 for (uint32_t given = 0; ok; ++given) {
@@ -382,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&B.item_full[slot]);
                     if (it.head < 0)
                         break;
-                    const int after = (int)gridDim.x + atomicAdd(&a.header[1], 1);
+                    // (a batch that is not listed has a CTA for every item)
+                    const int after = a.listed ? (int)gridDim.x + atomicAdd(&a.plan.header[1], 1) : items;
                     const int n0 = it.tiles0(), n1 = it.tiles1(), n = max(n0, n1);
                     if (n == 0) {
                         next = look_up(after);
@@ -736,7 +740,7 @@ cudaError_t launch(const Call &c)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = c.args.listed ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, c.maps, c.args);
 }
 
@@ -865,11 +869,13 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     pa.tiles = reinterpret_cast<ragged::Tile *>(ws + ragged::kPlanHeader);
     pa.err = device_error;
     c.stream = static_cast<cudaStream_t>(stream);
-    if (ragged::launch_plan(pa, c.stream) != cudaSuccess)
+    c.most_items = pa.capacity * H;
+    const bool listed = !ragged::small_plan(pa.batch, pa.capacity) || c.most_items > sm_count();
+    if (listed && ragged::launch_plan(pa, c.stream) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     PrefillArgs &a = c.args;
-    a.header = pa.header;
-    a.tiles = pa.tiles;
+    a.plan = pa;
+    a.listed = listed;
     a.out = out;
     a.lse = lse;
     a.err = device_error;
@@ -887,7 +893,6 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     // is taken as one too small to show in any weight
     a.scale_log2 = sm_scale == 0.f ? 1e-30f : fabsf(sm_scale) * 1.4426950408889634f;
     a.negate = sm_scale < 0.f ? 1u << 13 : 0u;
-    c.most_items = pa.capacity * H;
 
     const int nkn = (p->d_nope + 63) / 64, nvb = (p->d_v + 63) / 64;
     const bool rope = p->d_rope > 0;

@@ -26,29 +26,17 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanArgs a)
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     count[tid] = 0;
     static_assert(kClasses == kThreads, "one class a thread");
-    // rows and keys of sequence b; a range that runs backwards or out of the
-    // arrays is taken as empty
-    auto ranges = [&](int b, int &q0, int &nq, int &k0, int &nk) -> bool {
-        q0 = a.q_start[b];
-        const int q1 = a.q_start[b + 1];
-        k0 = a.kv_start[b];
-        const int k1 = a.kv_start[b + 1];
-        const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.max_q && k0 >= 0 && k0 <= k1 && k1 <= a.max_kv;
-        nq = ok ? q1 - q0 : 0;
-        nk = ok ? k1 - k0 : 0;
-        return ok;
-    };
     long long tiles = 0, total;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
         int q0, nq, k0, nk;
-        bad |= !ranges(b, q0, nq, k0, nk);
+        bad |= !ranges(a, b, q0, nq, k0, nk);
         tiles += (nq + a.rows_per_tile - 1) / a.rows_per_tile;
     }
     long long at = block_scan(tiles, total, sh_scan);
     for (int b = b0; b < b1; ++b) {
         int q0, nq, k0, nk;
-        ranges(b, q0, nq, k0, nk);
+        ranges(a, b, q0, nq, k0, nk);
         start[b] = (int)min(at, (long long)a.capacity);
         at += (nq + a.rows_per_tile - 1) / a.rows_per_tile;
     }
@@ -69,16 +57,8 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanArgs a)
     auto tile_of = [&](int i, Tile &t) -> int {
         const int b = find(start, a.batch, i);
         int q0, nq, k0, nk;
-        ranges(b, q0, nq, k0, nk);
-        const int off = (i - start[b]) * a.rows_per_tile;
-        t.q0 = q0 + off;
-        t.nq = min(nq - off, a.rows_per_tile);
-        t.k0 = k0;
-        t.nk = nk;
-        t.lim0 = a.causal ? nk - nq + off + 1 : nk;
-        t.seq = b;
-        t.tok0 = off;
-        t.pad = 0;
+        ranges(a, b, q0, nq, k0, nk);
+        t = make_tile(a, b, q0, nq, k0, nk, (i - start[b]) * a.rows_per_tile);
         const int last = a.causal ? min(nk, max(t.lim0 + t.nq - 1, 0)) : nk;
         return kClasses - 1 - (((last + 127) / 128) >> shift);
     };

@@ -108,6 +108,69 @@ struct PlanArgs {
     int32_t *err;
 };
 
+// Rows and keys of sequence b.  A range that runs backwards or out of the
+// arrays is taken as empty (false).
+__device__ __forceinline__ bool ranges(const PlanArgs &a, int b, int &q0, int &nq, int &k0, int &nk)
+{
+    q0 = a.q_start[b];
+    const int q1 = a.q_start[b + 1];
+    k0 = a.kv_start[b];
+    const int k1 = a.kv_start[b + 1];
+    const bool ok = q0 >= 0 && q0 <= q1 && q1 <= a.max_q && k0 >= 0 && k0 <= k1 && k1 <= a.max_kv;
+    nq = ok ? q1 - q0 : 0;
+    nk = ok ? k1 - k0 : 0;
+    return ok;
+}
+
+// Tile of the rows from `off` on of sequence b.
+__device__ __forceinline__ Tile make_tile(const PlanArgs &a, int b, int q0, int nq, int k0, int nk, int off)
+{
+    Tile t;
+    t.q0 = q0 + off;
+    t.nq = min(nq - off, a.rows_per_tile);
+    t.k0 = k0;
+    t.nk = nk;
+    t.lim0 = a.causal ? nk - nq + off + 1 : nk;
+    t.seq = b;
+    t.tok0 = off;
+    t.pad = 0;
+    return t;
+}
+
+// Small batches: their tiles, in the sequences' order, listed by one warp of
+// every CTA in its shared memory.  It saves the plan's launch (two 512-token
+// prompts of 8 heads: 16.2 -> 14.1 us on the device, the call on the host 9.5 ->
+// 5.5).
+constexpr int kSmallBatch = 32, kSmallTiles = 16;
+
+inline bool small_plan(int batch, long long capacity) { return batch <= kSmallBatch && capacity <= kSmallTiles; }
+
+// Returns the number of tiles (to every lane).  tiles: room for kSmallTiles.
+__device__ __forceinline__ int list_tiles(const PlanArgs &a, Tile *tiles, bool report)
+{
+    const int lane = threadIdx.x & 31;
+    int q0 = 0, nq = 0, k0 = 0, nk = 0;
+    const bool ok = lane >= a.batch || ranges(a, lane, q0, nq, k0, nk);
+    const int mine = (nq + a.rows_per_tile - 1) / a.rows_per_tile;
+    // overlapping ranges can ask for more tiles than there is room for
+    int at = min(mine, kSmallTiles + 1);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o)
+            at += x;
+    }
+    const int total = __shfl_sync(0xffffffffu, at, 31);
+    at -= min(mine, kSmallTiles + 1);
+    for (int i = 0; i < mine && at + i < a.capacity; ++i)
+        tiles[at + i] = make_tile(a, lane, q0, nq, k0, nk, i * a.rows_per_tile);
+    const bool bad = __any_sync(0xffffffffu, !ok) || total > a.capacity;
+    if (bad && report && lane == 0 && a.err)
+        atomicOr(a.err, KVATTN_DEVERR_BAD_LENGTH);
+    __syncwarp();
+    return min(total, a.capacity);
+}
+
 // Most tiles a batch can have: every sequence may end in one of its own.
 inline long long tile_capacity(long long rows, int batch, int rows_per_tile)
 {

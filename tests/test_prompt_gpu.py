@@ -327,6 +327,8 @@ def check_expand(got, cache, table, uk, uv, groups, lens, mpps):
     (4, 1, 512, 64, 128, 128, [1, 0, 63, 64, 65, 127, 128, 129, 300], True),
     (8, 2, 256, 64, 128, 128, [200, 1], True),
     (6, 2, 128, 32, 64, 128, [130, 0, 70], True),
+    (2, 1, 128, 16, 64, 64, [64] * 33, True),
+    (4, 2, 64, 64, 128, 128, [2000, 1, 500], True),
     (3, 1, 64, 16, 40, 72, [100, 129], False),
     (2, 1, 64, 0, 8, 8, [257], True),
     (130, 1, 64, 64, 128, 64, [64, 64], True),
@@ -439,10 +441,12 @@ LENS = [([1], [1]), ([1], [200]), ([127], [127]), ([128], [128]), ([129], [129])
 
 @pytest.mark.parametrize("ql,kl", LENS)
 @pytest.mark.parametrize("causal", [True, False])
-def test_prefill_lengths(dev, ql, kl, causal):
-    """Lengths around the tiles, cached prefixes, sequences without queries or keys, rows whose mask leaves nothing."""
+@pytest.mark.parametrize("slack", [9, 5000])
+def test_prefill_lengths(dev, ql, kl, causal, slack):
+    """Lengths around the tiles, cached prefixes, sequences without queries or keys, rows whose mask leaves nothing.
+    With little room for rows every CTA lists the tiles, with much the plan kernel does."""
     rng = np.random.default_rng(sum(ql) + sum(kl))
-    x = prefill_case(rng, 2, 2, 128, 64, 128, ql, kl)
+    x = prefill_case(rng, 2, 2, 128, 64, 128, ql, kl, slack)
     err = word(dev)
     got = call(dev, x, ql, kl, 192 ** -0.5, causal, device_error=err)
     assert int(err.item()) == 0
@@ -562,15 +566,23 @@ def test_prefill_nothing_passes_between_sequences(dev):
 
 
 def test_prefill_bad_starts_set_the_bit(dev):
+    import torch
     rng = np.random.default_rng(16)
     x = prefill_case(rng, 1, 1, 64, 0, 64, [50, 60, 70], [50, 60, 70])
     t = {k: None if v is None else up(v, dev) for k, v in x.items()}
-    for q, k in (([0, 50, 110, 400], [0, 50, 110, 180]), ([0, 50, 110, 180], [0, 50, 110, 400]),
-                 ([0, 50, 110, 90], [0, 50, 110, 180]), ([0, 50, 110, 180], [0, 50, 110, 90])):
-        err = word(dev)
-        got = K.prefill_tensors(t["q"], None, t["k"], None, t["v"], i32(q, dev), i32(k, dev), 0.1, device_error=err)
-        assert int(err.item()) == K.KVATTN_DEVERR_BAD_LENGTH
-        check_prefill(got, x, [50, 60], [50, 60], 0.1, True)
+    for room in (0, 5000):
+        t["q"] = torch.cat([t["q"], torch.zeros(room, 1, 64, dtype=torch.bfloat16, device=dev)])
+        far = 6000
+        for q, k in (([0, 50, 110, far], [0, 50, 110, 180]), ([0, 50, 110, 180], [0, 50, 110, far]),
+                     ([0, 50, 110, 90], [0, 50, 110, 180]), ([0, 50, 110, 180], [0, 50, 110, 90])):
+            check_bad_starts(dev, x, t, q, k)
+
+
+def check_bad_starts(dev, x, t, q, k):
+    err = word(dev)
+    got = K.prefill_tensors(t["q"], None, t["k"], None, t["v"], i32(q, dev), i32(k, dev), 0.1, device_error=err)
+    assert int(err.item()) == K.KVATTN_DEVERR_BAD_LENGTH
+    check_prefill(got, x, [50, 60], [50, 60], 0.1, True)
 
 
 def test_prefill_many_sequences(dev):
