@@ -499,8 +499,8 @@ int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cac
  * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded to
  * bf16 for the product with v.  Key and value rows of other sequences and past
  * the last one never reach a result, whatever they hold; inside a sequence
- * values are taken to be finite (a value that is not may reach queries up to
- * 127 tokens before it).
+ * values are taken to be finite (a value that is not may reach the up to 95
+ * queries before it).
  * workspace: kvattn_prefill_workspace_size bytes, 256-byte aligned, in any
  * state; calls that may run at the same time need one each.
  */
