@@ -16,8 +16,9 @@
 // its next scores are formed while its softmax runs (the scores' columns are
 // free as soon as they are in registers), and the other query tile's MMAs fill
 // what is left.  Measured: 1150 cycles per key tile and query tile (1056 of
-// MMAs) in the middle of an 8K prompt; the whole call, causal, 128 heads, runs
-// at 1.38 PFLOP/s from a cold start and at 1.2 when repeated, at the power cap.
+// MMAs) in the middle of an 8K prompt; the whole call, causal, 128 heads, takes
+// 1.90 ms from a cold start (1.45 PFLOP/s) and 2.2 ms when repeated, at the power
+// cap.
 // Forming a part of the exponentials on the FMA pipe makes the softmax shorter
 // and the call longer (8K prompt 2263 us without, 2321 with a quarter of them).
 //
@@ -38,8 +39,8 @@
 //              in fp32 (base 2), probabilities back to TMEM in bf16, output
 //              rescaled when the maximum grows by more than 2^8 (lazily: the
 //              reference maximum only scales numerator and denominator alike)
-// P is rounded to bf16 for the MMA (relative 2^-9, as in the decode kernels);
-// the sum uses the unrounded values; scores, maxima, sums and outputs stay in
+// P is rounded to bf16 for the MMA, as in the decode kernels (off by at most 2^-8
+// of the weight, as much as the output's own rounding); the sum uses the unrounded values; scores, maxima, sums and outputs stay in
 // fp32.
 //
 // The work list (tiles by falling number of keys) comes from ragged.cu; the
@@ -80,7 +81,7 @@ constexpr int kLaunchRegs = 168, kIssueRegs = 88, kSoftmaxRegs = 208;
 static_assert(kIssueRegs + 2 * kSoftmaxRegs <= 3 * kLaunchRegs, "register split");
 constexpr int kQBox = kTile * 128;                // 128 query rows x 64 bf16
 constexpr int kBox = kKeys * 128;                 // 96 keys x 64 bf16
-constexpr int kHeadGroup = 8, kLastHeads = 16;
+constexpr int kHeadGroup = 8, kLastHeads = 16;    // heads of a group, and at least in the last one
 constexpr int kBarBytes = 1024;
 constexpr int kSmemMax = 227 * 1024;
 
