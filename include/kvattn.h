@@ -464,8 +464,9 @@ int kvattn_append_slots(int32_t variant, const kvattn_params *p, const void *new
  * 64; d_k and d_v multiples of 8, at most 128.  A page id outside
  * [0, num_pages) sets KVATTN_DEVERR_PAGE_OUT_OF_RANGE; its tokens' keys and
  * values are 0.  k_rope may be NULL when d_rope == 0.
- * workspace: kvattn_expand_workspace_size bytes, 256-byte aligned, in any
- * state; calls that may run at the same time need one each.
+ * workspace: kvattn_expand_workspace_size bytes (0 for small batches: it may be
+ * NULL), 256-byte aligned, in any state; calls that may run at the same time need
+ * one each.
  */
 int kvattn_expand_workspace_size(int32_t variant, const kvattn_params *p, int32_t max_kv_tokens, size_t *bytes);
 int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cache, const int32_t *block_table,
@@ -501,8 +502,9 @@ int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cac
  * the last one never reach a result, whatever they hold; inside a sequence
  * values are taken to be finite (a value that is not may reach the up to 95
  * queries before it).
- * workspace: kvattn_prefill_workspace_size bytes, 256-byte aligned, in any
- * state; calls that may run at the same time need one each.
+ * workspace: kvattn_prefill_workspace_size bytes (0 for small problems: it may be
+ * NULL), 256-byte aligned, in any state; calls that may run at the same time need
+ * one each.
  */
 typedef struct {
     int32_t batch;             /* sequences, 1..16384 */

@@ -507,8 +507,8 @@ extern "C" int kvattn_expand_workspace_size(int32_t variant, const kvattn_params
         return KVATTN_ERR_INVALID_ARG;
     if (!pr.latent || max_kv_tokens > ragged::kMaxRows)
         return KVATTN_ERR_UNSUPPORTED;
-    *bytes = ragged::kPlanHeader +
-             (size_t)ragged::tile_capacity(max_kv_tokens, p->batch, kRows) * sizeof(ragged::Tile);
+    const long long cap = ragged::tile_capacity(max_kv_tokens, p->batch, kRows);
+    *bytes = ragged::small_plan(p->batch, cap) ? 0 : ragged::kPlanHeader + (size_t)cap * sizeof(ragged::Tile);
     return KVATTN_OK;
 }
 
@@ -524,7 +524,7 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
         return st;
     Problem pr;
     validate_params(variant, p, &pr);
-    if (!kv_cache || !kv_start || !w_uk || !w_uv || !k_nope || !v || !workspace || (pr.dr > 0 && !k_rope) ||
+    if (!kv_cache || !kv_start || !w_uk || !w_uv || !k_nope || !v || (need && !workspace) || (pr.dr > 0 && !k_rope) ||
         d_k < 1 || d_v < 1)
         return KVATTN_ERR_INVALID_ARG;
     if (d_k % 8 || d_v % 8 || d_k > 128 || d_v > 128 || pr.dn % 64 || p->batch > ragged::kMaxBatch ||

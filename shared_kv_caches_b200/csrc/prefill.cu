@@ -731,9 +731,9 @@ cudaError_t launch(const Call &c)
     }(reinterpret_cast<const void *>(kern));
     if (regs != kLaunchRegs)
         return cudaErrorInvalidConfiguration;
-    const long long sms = sm_count();
+    const long long most = c.args.listed ? sm_count() : c.most_items;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(c.most_items < sms ? c.most_items : sms));
+    cfg.gridDim = dim3((unsigned)(c.most_items < most ? c.most_items : most));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = c.stream;
@@ -764,6 +764,14 @@ bool rows_map(CUtensorMap *map, const void *x, int d, int heads, long long token
     const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, bytes, box,
                         CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+// Whether the plan kernel lists the tiles.  Else every item has a CTA of its
+// own, and every CTA lists them: up to as many as a B200 runs at once.
+bool needs_plan(const kvattn_prefill_params *p)
+{
+    const long long cap = ragged::tile_capacity(p->max_q_tokens, p->batch, kItemRows);
+    return !ragged::small_plan(p->batch, cap) || cap * p->num_q_heads > kDefaultSMs;
 }
 
 int validate_prefill(const kvattn_prefill_params *p)
@@ -797,8 +805,9 @@ extern "C" int kvattn_prefill_workspace_size(const kvattn_prefill_params *p, siz
         return st;
     if (!bytes)
         return KVATTN_ERR_INVALID_ARG;
-    *bytes = ragged::kPlanHeader +
-             (size_t)ragged::tile_capacity(p->max_q_tokens, p->batch, kItemRows) * sizeof(ragged::Tile);
+    *bytes = !needs_plan(p) ? 0
+                            : ragged::kPlanHeader + (size_t)ragged::tile_capacity(p->max_q_tokens, p->batch, kItemRows) *
+                                                        sizeof(ragged::Tile);
     return KVATTN_OK;
 }
 
@@ -812,7 +821,7 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     if (st)
         return st;
     const bool keys = p->max_kv_tokens > 0;      // without any, key and value pointers may be null
-    if (!q_nope || !q_start || !kv_start || !out || !workspace || (keys && (!k_nope || !v)) ||
+    if (!q_nope || !q_start || !kv_start || !out || (need && !workspace) || (keys && (!k_nope || !v)) ||
         (p->d_rope > 0 && (!q_rope || (keys && !k_rope))) || !isfinite(sm_scale))
         return KVATTN_ERR_INVALID_ARG;
     if (!is_aligned(q_nope, 16) || !is_aligned(q_rope, 16) || !is_aligned(k_nope, 16) || !is_aligned(k_rope, 16) ||
@@ -871,7 +880,7 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     pa.err = device_error;
     c.stream = static_cast<cudaStream_t>(stream);
     c.most_items = pa.capacity * H;
-    const bool listed = !ragged::small_plan(pa.batch, pa.capacity) || c.most_items > sm_count();
+    const bool listed = needs_plan(p);
     if (listed && ragged::launch_plan(pa, c.stream) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     PrefillArgs &a = c.args;

@@ -453,10 +453,10 @@ def expand_kv_tensors(variant, params, kv_cache, block_table, kv_start, w_uk, w_
     k_rope = kv_cache.new_empty((n, dr)) if dr else None
     if n:
         ws_bytes = kvattn_expand_workspace_size(variant, params, n)
-        ws = kv_cache.new_empty(ws_bytes // 2)
+        ws = kv_cache.new_empty(ws_bytes // 2) if ws_bytes else None
         _enqueue("kvattn_expand_kv", dev, load().kvattn_expand_kv, int(variant), ctypes.byref(params),
                  kv_cache.data_ptr(), _ptr(block_table), kv_start.data_ptr(), n, d_k, d_v, w_uk.data_ptr(),
-                 w_uv.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_rope), ws.data_ptr(), ws_bytes,
+                 w_uv.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_rope), _ptr(ws), ws_bytes,
                  _error_word(device_error, dev))
     return dict(k=k, v=v, k_rope=k_rope)
 
@@ -507,8 +507,8 @@ def prefill_tensors(q_nope, q_rope, k, k_rope, v, q_start, kv_start, sm_scale, c
                                   (rs[0] * t1, rs[1] * h1), (ks[1] * k1, ks[0] * kh1), (vs[1] * k1, vs[0] * kh1),
                                   (os[0] * t1, os[1] * h1), krs * k1)
         ws_bytes = kvattn_prefill_workspace_size(p)
-        ws = q_nope.new_empty(ws_bytes // 2)
+        ws = q_nope.new_empty(ws_bytes // 2) if ws_bytes else None
         _enqueue("kvattn_prefill", dev, load().kvattn_prefill, ctypes.byref(p), q_nope.data_ptr(), _ptr(q_rope),
                  k.data_ptr(), _ptr(k_rope), v.data_ptr(), q_start.data_ptr(), kv_start.data_ptr(), sm_scale,
-                 out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws_bytes, _error_word(device_error, dev))
+                 out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes, _error_word(device_error, dev))
     return dict(out=out, lse=lse)

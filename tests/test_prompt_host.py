@@ -67,7 +67,7 @@ def test_append_refusals(lib, kw, status):
 EXPAND_PTRS = ["cache", "table", "start", "uk", "uv", "k", "v", "kr", "ws"]
 
 
-def expand(variant=K.KVATTN_MLA, n=500, d_k=128, d_v=128, ws_bytes=1 << 30, err=None, ptr=None, **kw):
+def expand(variant=K.KVATTN_MLA, n=5000, d_k=128, d_v=128, ws_bytes=1 << 30, err=None, ptr=None, **kw):
     d = dict(batch=2, num_q_heads=16, num_kv=1, d_nope=512, d_rope=64, max_pages_per_seq=4, num_pages=9, max_seq_len=0)
     d.update(kw)
     x = {k: FAKE for k in EXPAND_PTRS} | (ptr or {})
@@ -94,7 +94,7 @@ def test_expand_null_and_misaligned_pointers(lib, name):
 
 # ----------------------------------------------------------------- prefill
 def params(**kw):
-    d = dict(batch=2, num_q_heads=8, num_kv_heads=4, d_nope=128, d_rope=64, d_v=128, max_q_tokens=500, max_kv_tokens=700,
+    d = dict(batch=2, num_q_heads=8, num_kv_heads=4, d_nope=128, d_rope=64, d_v=128, max_q_tokens=5000, max_kv_tokens=7000,
              causal=1, out_dtype=0, num_q_nope_heads=0)
     d.update({k: v for k, v in kw.items() if not k.endswith("stride")})
     p = K.kvattn_prefill_params(*d.values())
@@ -137,9 +137,24 @@ def test_prefill_null_and_misaligned_pointers(lib, name):
 
 
 def test_workspace_sizes_cover_a_tile_for_every_sequence(lib):
-    assert K.kvattn_prefill_workspace_size(params(batch=3, max_q_tokens=513)) >= 32 * (3 + 3)
+    assert K.kvattn_prefill_workspace_size(params(batch=3, max_q_tokens=5121)) >= 32 * (21 + 3)
     p = K.make_params(5, 16, 1, 512, 64, 4, 9, 0)
-    assert K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, 129) >= 32 * (2 + 5)
+    assert K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, 12900) >= 32 * (101 + 5)
+
+
+def test_small_batches_need_no_workspace(lib):
+    """Up to 32 sequences and 16 tiles (and, for attention, an item for each SM at most)."""
+    p = K.make_params(5, 16, 1, 512, 64, 4, 9, 0)
+    assert K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, 128 * 11) == 0
+    assert K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, 128 * 11 + 1) > 0
+    assert K.kvattn_prefill_workspace_size(params(max_q_tokens=256 * 14)) == 0
+    assert K.kvattn_prefill_workspace_size(params(max_q_tokens=256 * 14 + 1)) > 0
+    assert K.kvattn_prefill_workspace_size(params(max_q_tokens=256, num_q_heads=64)) > 0
+    assert K.kvattn_prefill_workspace_size(params(batch=33, max_q_tokens=33, num_q_heads=4)) > 0
+
+
+def test_workspace_sizes_refuse_what_the_calls_refuse(lib):
+    p = K.make_params(5, 16, 1, 512, 64, 4, 9, 0)
     with pytest.raises(K.KvattnError):
         K.kvattn_expand_workspace_size(K.KVATTN_MLA, p, -1)
 
