@@ -498,10 +498,9 @@ int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cac
  * inputs; out bf16 (nearest even) or fp32.  d_nope and d_v multiples of 8 up to
  * 128, d_rope of 8 up to 64.
  * Scores, maxima, sums and outputs are fp32; the softmax weights are rounded to
- * bf16 for the product with v.  Key and value rows of other sequences and past
- * the last one never reach a result, whatever they hold; inside a sequence
- * values are taken to be finite (a value that is not may reach the up to 95
- * queries before it).
+ * bf16 for the product with v.  What a query's mask leaves out, and key and value
+ * rows of other sequences or past the last one, never reaches its result,
+ * whatever it holds.
  * workspace: kvattn_prefill_workspace_size bytes (0 for small problems: it may be
  * NULL), 256-byte aligned, in any state; calls that may run at the same time need
  * one each.

@@ -35,6 +35,8 @@
 //   warp 2     issues those of P.V, PV0(j) PV1(j) PV0(j+1) ... (a warp of its
 //              own: one that issued both spent more time on the waits and
 //              commits between them than the MMAs take)
+//   warp 3     guards the value tiles that some row does not attend whole: what
+//              is not finite there must not reach the rows that leave it out
 //   warps 4-11 one thread per query row: scores from TMEM, mask, online softmax
 //              in fp32 (base 2), probabilities back to TMEM in bf16, output
 //              rescaled when the maximum grows by more than 2^8 (lazily: the
@@ -82,7 +84,7 @@ static_assert(kIssueRegs + 2 * kSoftmaxRegs <= 3 * kLaunchRegs, "register split"
 constexpr int kQBox = kTile * 128;                // 128 query rows x 64 bf16
 constexpr int kBox = kKeys * 128;                 // 96 keys x 64 bf16
 constexpr int kHeadGroup = 8, kLastHeads = 16;    // heads of a group, and at least in the last one
-constexpr int kBarBytes = 1024;
+constexpr int kBarBytes = 2048;
 constexpr int kSmemMax = 227 * 1024;
 
 struct PrefillArgs {
@@ -96,6 +98,8 @@ struct PrefillArgs {
     int d_v, out_fp32, causal;
     int wide;                                     // output rows start on 32 bytes
     long long out_token_stride, out_head_stride;
+    const __nv_bfloat16 *v;
+    long long v_token_stride, v_head_stride;
     float scale_log2;                             // of the scale's magnitude
     uint32_t negate;                              // a negative scale: the MMAs take -q (the instruction descriptor's bit)
 };
@@ -121,18 +125,25 @@ struct Item {
     int32_t head;                                 // -1: no more items
     int32_t end0, end1;                           // keys that the last row of each query tile attends
 
+    int32_t all;                                  // keys that every row attends
+
     __device__ __forceinline__ int tiles0() const { return (end0 + kKeys - 1) / kKeys; }
     __device__ __forceinline__ int tiles1() const { return (end1 + kKeys - 1) / kKeys; }
 };
 
 // The items that the TMA thread hands out stand here until all have read them.
 constexpr int kItems = 4;
-constexpr int kItemReaders = 10;                  // the MMA warps and the softmax warps
+constexpr int kItemReaders = 11;                  // the MMA, guard and softmax warps
+// Key tiles of an item that some row does not attend, or that end behind the
+// sequence: the rows' limits span 256 keys.
+constexpr int kEdgeTiles = 5;
 
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
+    uint32_t bad[kItems][kEdgeTiles][kKeys / 32]; // tokens of the edge tiles whose values are not finite
+    uint64_t edge_full[2];                        // an edge tile's values have landed (the guard looks them over)
     ragged::Tile tiles[ragged::kSmallTiles];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], s_free[2];                // scores formed; scores in registers
@@ -199,6 +210,16 @@ __device__ __forceinline__ int key_end(const PrefillArgs &a, const ragged::Tile 
     return a.causal ? min(t.nk, max(t.lim0 + rows_before + rows - 1, 0)) : t.nk;
 }
 
+// Of two bf16 values: the top bit of each that is infinite or NaN; and the word
+// with those set to 0.
+__device__ __forceinline__ uint32_t exponent_ones(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+__device__ __forceinline__ uint32_t finite_only(uint32_t w)
+{
+    const uint32_t e = exponent_ones(w);
+    return w & ~((e & 0x8000u ? 0xffffu : 0u) | (e & 0x80000000u ? 0xffff0000u : 0u));
+}
+
 // N words of a row: with `wide` (rows that start on 32 bytes) a whole sector at a time.
 template <int N>
 __device__ __forceinline__ void store_row(void *p, const uint32_t *r, bool wide)
@@ -231,6 +252,7 @@ __device__ __forceinline__ Item get_item(const PrefillArgs &a, const ragged::Til
     it.head = g * kHeadGroup + r % hc;
     it.end0 = key_end(a, t, 0, min(t.nq, kTile));
     it.end1 = key_end(a, t, kTile, t.nq - kTile);
+    it.all = a.causal ? min(t.nk, max(t.lim0 + (it.end0 > 0 ? 0 : kTile), 0)) : t.nk;
     return it;
 }
 
@@ -257,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B.k_empty[i], 1);
             mbar_init(&B.v_full[i], 1);
             mbar_init(&B.v_empty[i], 1);
+            mbar_init(&B.edge_full[i], 1);
             mbar_init(&B.q_full[i], 1);
             mbar_init(&B.q_empty[i], 1);
             mbar_init(&B.s_full[i], 1);
@@ -317,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 uint32_t kn = 0, vn = 0;                     // key and value tiles loaded
                 uint32_t qn[2] = {0, 0};                     // query tiles loaded
+                uint32_t edge_seen = 0;                      // bit st: an edge tile was loaded; bit 2 + st: an odd number
                 auto load_q = [&](const Item &it, int i) {
                     if (qn[i] > 0 && !mbar_wait(&B.q_empty[i], (qn[i] - 1) & 1)) {
                         ok = false;
@@ -359,10 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ++vn;
                     unsigned char *dst = smem + Lay::kValuesAt + st * Lay::kValueTile;
-                    mbar_arrive_expect_tx(&B.v_full[st], Lay::kValueTile);
+                    const bool edge = (j + 1) * kKeys > it.all;
+                    if (edge)
+                        edge_seen = (edge_seen | 1u << st) ^ 4u << st;
+                    uint64_t *const full = edge ? &B.edge_full[st] : &B.v_full[st];
+                    mbar_arrive_expect_tx(full, Lay::kValueTile);
 #pragma unroll
                     for (int b = 0; b < NVB; ++b)
-                        tma_load_3d(dst + b * kBox, &m.v, 64 * b, kvh, row, &B.v_full[st]);
+                        tma_load_3d(dst + b * kBox, &m.v, 64 * b, kvh, row, full);
                 };
                 // items are handed out as CTAs get to them: the first by the block's
                 // number, then by a count that the plan kernel sets to 0
@@ -414,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kn > st && !mbar_wait(&B.k_full[st], ((kn - 1 - st) >> 1) & 1))
                         ok = false;
                     if (vn > st && !mbar_wait(&B.v_full[st], ((vn - 1 - st) >> 1) & 1))
+                        ok = false;
+                    if ((edge_seen >> st & 1) && !mbar_wait(&B.edge_full[st], (edge_seen >> (2 + st) & 1) ^ 1))
                         ok = false;
                     if (qn[st] > 0 && !mbar_wait(&B.q_full[st], (qn[st] - 1) & 1))
                         ok = false;
@@ -480,7 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ppar = 0;                               // phase bit i: probabilities of query tile i
             for (const Item *it; ok && (it = next_item());) {
                 const int end0 = __shfl_sync(0xffffffffu, it->end0, 0), end1 = __shfl_sync(0xffffffffu, it->end1, 0);
-                const int nk = __shfl_sync(0xffffffffu, it->nk, 0);
                 done_item();
                 const int n0 = (end0 + kKeys - 1) / kKeys, n1 = (end1 + kKeys - 1) / kKeys, n = max(n0, n1);
                 // the first to store probabilities waits for all items before
@@ -494,23 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     const uint32_t st = (t + j) & 1;
                     bool in = true;
-                    if (i == 0 || j >= other) {              // the first of the tile's uses
+                    if (i == 0 || j >= other)                // the first of the tile's uses
                         in = mbar_wait(&B.v_full[st], ((t + j) >> 1) & 1);
-                        // value rows past the sequence are zeroed: their
-                        // probabilities are 0, and 0 * NaN would poison the output
-                        const int ntok = nk - j * kKeys;
-                        if (ntok < kKeys) {
-                            in = __all_sync(0xffffffffu, in);
-                            unsigned char *v0 = smem + Lay::kValuesAt + st * Lay::kValueTile;
-                            for (int idx = lane; in && idx < (kKeys - ntok) * 8 * NVB; idx += 32) {
-                                const int b = idx / ((kKeys - ntok) * 8), rem = idx % ((kKeys - ntok) * 8);
-                                *reinterpret_cast<uint4 *>(v0 + b * kBox + (ntok + rem / 8) * 128 + (rem % 8) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
                     in = in && mbar_wait(&B.p_full[i], (ppar >> i) & 1);
                     ppar ^= 1u << i;
                     ok = __all_sync(0xffffffffu, in);
@@ -538,6 +552,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t += (uint32_t)n;
             }
             finish();
+        } else {
+            // -------------------------------------------------------------- guard
+            // Values that a row's mask leaves out have the weight 0, and 0 * NaN
+            // or 0 * infinity in P.V would still spoil it.  In the tiles that
+            // some row does not attend whole, rows past the sequence become 0,
+            // and so do values that are not finite; their tokens are noted, and
+            // the rows that do attend them add those values in the end.
+            uint32_t t = 0, epar = 0;                        // value tiles of the items before; phase bits of edge_full
+            for (const Item *it; ok && (it = next_item());) {
+                const int n = max(it->tiles0(), it->tiles1()), nk = it->nk, all = it->all;
+                uint32_t(*const bad)[kKeys / 32] = B.bad[taken % kItems];
+                if (lane < kEdgeTiles * (kKeys / 32))
+                    bad[lane / (kKeys / 32)][lane % (kKeys / 32)] = 0;
+                __syncwarp();
+                for (int j = all / kKeys; j < n; ++j) {
+                    const uint32_t st = (t + j) & 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&B.edge_full[st], (epar >> st) & 1));
+                    if (!ok)
+                        break;
+                    epar ^= 1u << st;
+                    unsigned char *const v0 = smem + Lay::kValuesAt + st * Lay::kValueTile;
+                    // a 16-byte piece of four rows a lane, six times at once: P.V may be waiting
+                    const int tok0 = j * kKeys, ntok = min(nk - tok0, kKeys);
+                    auto piece = [&](int r, int b) -> uint4 * {
+                        return reinterpret_cast<uint4 *>(v0 + b * kBox + r * 128 + (lane & 7) * 16);
+                    };
+                    for (int r0 = max(all - tok0, 0) / 24 * 24; r0 < ntok; r0 += 24) {
+                        uint4 x[6][NVB];
+                        uint32_t ones = 0;
+#pragma unroll
+                        for (int y = 0; y < 6; ++y)
+#pragma unroll
+                            for (int b = 0; b < NVB; ++b)
+                                x[y][b] = *piece(r0 + 4 * y + (lane >> 3), b);
+#pragma unroll
+                        for (int y = 0; y < 6; ++y)
+#pragma unroll
+                            for (int b = 0; b < NVB; ++b)
+                                ones |= exponent_ones(x[y][b].x) | exponent_ones(x[y][b].y) | exponent_ones(x[y][b].z) |
+                                        exponent_ones(x[y][b].w);
+                        if (!__any_sync(0xffffffffu, ones != 0))
+                            continue;
+                        for (int y = 0; y < 6; ++y) {
+                            const int r = r0 + 4 * y + (lane >> 3);
+                            for (int b = 0; b < NVB; ++b) {
+                                const uint4 w = *piece(r, b);
+                                if (r < ntok && (exponent_ones(w.x) | exponent_ones(w.y) | exponent_ones(w.z) | exponent_ones(w.w))) {
+                                    *piece(r, b) = make_uint4(finite_only(w.x), finite_only(w.y), finite_only(w.z), finite_only(w.w));
+                                    atomicOr(&bad[j - all / kKeys][r >> 5], 1u << (r & 31));
+                                }
+                            }
+                        }
+                    }
+                    for (int idx = lane; idx < (kKeys - ntok) * 8 * NVB; idx += 32)    // (lane & 7: the column)
+                        *piece(ntok + idx / (8 * NVB), idx / 8 % NVB) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&B.v_full[st]);
+                }
+                t += (uint32_t)n;
+                done_item();
+            }
+            if (!ok && lane == 0 && a.err)
+                atomicOr(a.err, KVATTN_DEVERR_WAIT_TIMEOUT);
         }
     } else {
         set_regs_up<kSoftmaxRegs>();
@@ -649,7 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = row < it->nq;
             const int head = it->head;
             const long long grow = (long long)it->q0 + row;
-            done_item();
+            // values that are not finite, of tokens near the rows' ends: rare
+            uint32_t any_bad = 0;
+            for (int e = lane; e < kEdgeTiles * (kKeys / 32); e += 32)
+                any_bad |= B.bad[taken % kItems][e / (kKeys / 32)][e % (kKeys / 32)];
+            any_bad = __any_sync(0xffffffffu, any_bad != 0);
             const bool any = n > 0 && l != 0.f;          // a row without keys has l = 0 (NaN passes)
             const float inv = any ? 1.f / l : 0.f;
             const long long at = grow * a.out_token_stride + head * a.out_head_stride;
@@ -665,6 +748,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int y = 0; y < 64; ++y)
                     f[y] = any ? f[y] * inv : 0.f;
+                if (any_bad && n > 0) {
+                    // P.V took them as 0: the rows that attend their tokens get them here
+                    const int edge = it->all / kKeys;
+                    const __nv_bfloat16 *const v0 = a.v + (long long)it->k0 * a.v_token_stride +
+                                                    (head / a.heads_per_kv) * a.v_head_stride + x;
+#pragma unroll 1
+                    for (int e = 0; e < kEdgeTiles * kKeys; ++e) {
+                        const int tok = edge * kKeys + e;
+                        if (!(B.bad[taken % kItems][e / kKeys][e % kKeys / 32] >> (e % 32) & 1) || tok >= lim)
+                            continue;
+#pragma unroll
+                        for (int y = 0; y < 64; y += 8) {
+                            if (x + y >= a.d_v)
+                                continue;
+                            const uint4 u = *reinterpret_cast<const uint4 *>(v0 + tok * a.v_token_stride + y);
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const uint32_t ones = exponent_ones(w[z]);
+                                f[y + 2 * z] += ones & 0x8000u ? __uint_as_float(w[z] << 16) : 0.f;
+                                f[y + 2 * z + 1] += ones & 0x80000000u ? __uint_as_float(w[z] & 0xffff0000u) : 0.f;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
                 if (valid && x < a.d_v) {
                     if (a.out_fp32) {
                         float *const dst = static_cast<float *>(a.out) + at + x;
@@ -693,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (valid && a.lse)
                 a.lse[grow * a.heads + head] = any ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+            done_item();
             // the next item's first P.V overwrites the output: it follows this
             // warp's next arrival, which follows these loads
             tc_fence_before();
@@ -899,6 +1009,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     a.wide = is_aligned(out, 32) && so[0] % (a.out_fp32 ? 8 : 16) == 0 && so[1] % (a.out_fp32 ? 8 : 16) == 0;
     a.out_token_stride = so[0];
     a.out_head_stride = so[1];
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.v_token_stride = sv[0];
+    a.v_head_stride = sv[1];
     // masked scores are infinite, so a scale of 0 (every key weighs the same)
     // is taken as one too small to show in any weight
     a.scale_log2 = sm_scale == 0.f ? 1e-30f : fabsf(sm_scale) * 1.4426950408889634f;

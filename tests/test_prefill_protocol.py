@@ -1,7 +1,7 @@
 """Protocol model of the prefill kernel (csrc/prefill.cu), without a GPU.
 
 The agents are the kernel's: the TMA thread, the warp that issues the scores'
-MMAs, the one that issues P.V, and the softmax warps of both query tiles.  TMA
+MMAs, the one that issues P.V, the guard, and the softmax warps of both query tiles.  TMA
 landings come in any order; each issuing warp's MMAs and commits run in order,
 the two warps' in any interleaving.  mbarriers follow the hardware's rules
 (arrivals, transaction bytes, phases told apart by their parity alone), and
@@ -9,6 +9,9 @@ every wait says which phase it means: one that passes early is an error.  Every
 read is checked for the tile it expects, every write for readers that are not
 done.  Random interleavings of small items (several, of different lengths, with
 query tiles without keys) must end without deadlock; planted mistakes must not.
+
+Values of tiles that some row does not attend whole (the last ones of an item)
+land on a barrier of the guard warp, which looks them over before P.V may.
 """
 
 import random
@@ -56,7 +59,7 @@ class Model:
     def __init__(self, items, rng, broken=None):
         self.items, self.rng, self.broken = items, rng, broken
         B = Bar
-        self.bar = dict(item_full=[B(1) for _ in range(ITEMS)], item_empty=[B(2 + 2 * WARPS) for _ in range(ITEMS)],
+        self.bar = dict(item_full=[B(1) for _ in range(ITEMS)], item_empty=[B(3 + 2 * WARPS) for _ in range(ITEMS)], edge_full=[B(1), B(1)],
                         k_full=[B(1), B(1)], k_empty=[B(1), B(1)], v_full=[B(1), B(1)], v_empty=[B(1), B(1)],
                         q_full=[B(1), B(1)], q_empty=[B(1), B(1)], s_full=[B(1), B(1)], s_free=[B(WARPS), B(WARPS)],
                         p_full=[B(WARPS), B(WARPS)], p_free=[B(1), B(1)], o_full=[B(1), B(1)])
@@ -150,7 +153,8 @@ class Model:
                 if vn >= 2:
                     yield ("v_empty", st, (vn >> 1) - 1, (vn >> 1) - 1)
                 vn += 1
-                self.load("V", st, (given, j), bar["v_full"][st])
+                edge = j >= self.edge(given)
+                self.load("V", st, (given, j, "raw") if edge else (given, j), bar["edge_full" if edge else "v_full"][st])
             if n == 0:
                 continue
             if n0:
@@ -162,6 +166,32 @@ class Model:
                 if j + 1 < n:
                     yield from load_k(j + 1)
                 yield from load_v(j)
+
+    def edge(self, it):
+        """The first tile of the item that some row does not attend whole."""
+        n0, n1 = self.items[it]
+        return max((n0 if n0 else n1) - 2, 0)
+
+    def guard(self):
+        bar, t, taken, e = self.bar, 0, 0, [0, 0]
+        while True:
+            it = yield from self.take(taken)
+            if it < 0:
+                return
+            n = max(self.items[it])
+            for j in range(self.edge(it), n):
+                st = (t + j) & 1
+                if self.broken != "guard":
+                    yield ("edge_full", st, e[st], e[st])
+                e[st] += 1
+                check(self.V[st] == (it, j, "raw"), "the guard looks over another tile")
+                yield None
+                check(self.V[st] == (it, j, "raw") and self.readers.get(("V", st), 0) == 0, "values looked over while they are read")
+                self.V[st] = (it, j)
+                bar["v_full"][st].arrive()
+            t += n
+            bar["item_empty"][taken % ITEMS].arrive()
+            taken += 1
 
     def take(self, taken):
         yield ("item_full", taken % ITEMS, taken // ITEMS, taken // ITEMS)
@@ -276,7 +306,7 @@ class Model:
             taken += 1
 
     def run(self):
-        agents = [self.tma(), self.scores(), self.pv()] + [self.softmax(i, w) for i in range(2) for w in range(WARPS)]
+        agents = [self.tma(), self.scores(), self.pv(), self.guard()] + [self.softmax(i, w) for i in range(2) for w in range(WARPS)]
         waits = [None] * len(agents)
         live = set(range(len(agents)))
         for _ in range(200000):
@@ -323,7 +353,7 @@ def test_chosen_items_end_well(items):
         Model(items, random.Random(seed)).run()
 
 
-@pytest.mark.parametrize("broken", ["q_empty", "k_empty", "s_free", "p_free", "next", "o_full"])
+@pytest.mark.parametrize("broken", ["q_empty", "k_empty", "s_free", "p_free", "next", "o_full", "guard"])
 def test_planted_mistakes_are_caught(broken):
     caught = 0
     for seed in range(30):

@@ -565,6 +565,45 @@ def test_prefill_nothing_passes_between_sequences(dev):
         check_prefill(call(dev, x, ql, kl, 0.1, causal), x, ql, kl, 0.1, causal, skip=(1,))
 
 
+@pytest.mark.parametrize("ql,kl,at", [([200], [200], [0, 95, 96, 128, 150, 199]), ([300], [430], [130, 131, 300, 429]),
+                                      ([70, 260], [70, 500], [69, 100, 309, 333, 569]), ([40], [20], [0, 19]),
+                                      ([257], [257], [255, 256]), ([96], [1000], [900, 904, 905, 999])])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_prefill_values_that_are_not_finite(dev, ql, kl, at, fp32):
+    """A token whose value is NaN or infinite reaches the queries that attend it, in the columns that are, and no other."""
+    rng = np.random.default_rng(26)
+    x = prefill_case(rng, 3, 3, 128, 64, 128, ql, kl)
+    clean = {k: None if v is None else v.copy() for k, v in x.items()}
+    inf, ninf = 0x7F80, 0xFF80
+    for i, t in enumerate(at):
+        x["v"][i % 3, t, 5 * i:5 * i + 2] = W.BF16_NAN
+        x["v"][1, t, 70 + i], x["v"][2, t, 127 - i] = inf, ninf
+    x["k"][0, at[-1], 3] = W.BF16_NAN                       # a key: its queries' whole rows
+    for causal in (True, False):
+        got = call(dev, x, ql, kl, 0.07, causal, out_fp32=fp32)
+        ref = call(dev, clean, ql, kl, 0.07, causal, out_fp32=fp32)
+        out, lse, want, want_lse = (down(got["out"]), down(got["lse"]), down(ref["out"]), down(ref["lse"]))
+        qs, ks = starts(ql), starts(kl)
+        for b in range(len(ql)):
+            nq, nk = ql[b], kl[b]
+            for h in range(3):
+                v = f64(x["v"][h, ks[b]:ks[b + 1]])
+                for i in range(nq):
+                    n = min(nk, max(i + nk - nq + 1, 0)) if causal else nk
+                    row, line = out[qs[b] + i, h], want[qs[b] + i, h]
+                    if h == 0 and ks[b] <= at[-1] < ks[b] + n:
+                        assert np.isnan(row).all() and np.isnan(lse[qs[b] + i, h])
+                        continue
+                    with np.errstate(invalid="ignore"):
+                        add = np.where(np.isfinite(v[:n]), 0.0, v[:n]).sum(0) if n else np.zeros(128)
+                    np.testing.assert_array_equal(np.isnan(row), np.isnan(add))
+                    np.testing.assert_array_equal(row[np.isinf(add)], add[np.isinf(add)])
+                    fine = np.isfinite(add)
+                    # the other columns lose or gain nothing
+                    np.testing.assert_array_equal(row[fine], line[fine])
+                    assert lse[qs[b] + i, h] == want_lse[qs[b] + i, h]
+
+
 def test_prefill_bad_starts_set_the_bit(dev):
     import torch
     rng = np.random.default_rng(16)
