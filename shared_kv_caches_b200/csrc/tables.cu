@@ -383,7 +383,9 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
     const int most = in_place ? kTableMaxCtas : sm_count();
     ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
     const size_t smem = (3 * (size_t)batch + 2) * sizeof(int32_t);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    // the 48 KB of a launch without an opt-in hold what the kernel declares
+    // itself (272 bytes) too
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     cudaLaunchConfig_t cfg{};

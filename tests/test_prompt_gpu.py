@@ -806,3 +806,34 @@ def test_a_prompt_then_tokens(dev, name):
     assert len(last) == 2 and np.linalg.norm(one - two) <= 1.5e-2 * np.linalg.norm(two)
     # lse of the two forms: keys rounded to bf16 in one, the absorbed query in the other
     assert np.abs(down(lse) - down(got["lse"][idx])).max() <= 2e-2
+
+
+# ------------------------------------------------- sizes of a first call
+
+FRESH = """
+import sys
+import numpy as np, torch
+from oracle import prompt
+from shared_kv_caches_b200 import kvattn as K
+B = int(sys.argv[1])
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda:0")
+pages = B + 5
+free = np.random.default_rng(B).permutation(pages)
+table = np.full((B, 1), -1)
+r = K.build_tables_tensors(i32([0] * B), i32([1] * B), i32(free), i32([pages]), i32(table), B)
+ref = prompt.build_tables([0] * B, [1] * B, free, pages, table, B, pages)
+ref.pop("err")
+for k in ref:
+    assert np.array_equal(r[k].cpu().numpy(), ref[k]), k
+"""
+
+
+@pytest.mark.parametrize("batch", [4072, 4073, 4095, 4096])
+def test_tables_first_call_of_a_process(dev, batch):
+    """Batches around the 48 KB of shared memory that a launch may take without an opt-in."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH, str(batch)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
