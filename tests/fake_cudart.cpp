@@ -15,7 +15,7 @@ constexpr int kDefaultShared = 48 * 1024, kMostShared = 227 * 1024;
 
 struct Kernel {
     std::string name;
-    int opt_in = kDefaultShared;
+    int opt_in = -1;                   // bytes, once it has been set
     int fixed = 0;                     // declared shared memory, told by the test
 };
 
@@ -42,7 +42,7 @@ bool fails(const char *call)
 cudaError_t launched(const void *f, dim3 grid, dim3 block, size_t shared, unsigned cluster)
 {
     Kernel &k = kernels[f];
-    const bool fits = (int)shared + k.fixed <= (k.opt_in > kDefaultShared ? k.opt_in + k.fixed : kDefaultShared);
+    const bool fits = (int)shared <= (k.opt_in < 0 ? kDefaultShared - k.fixed : k.opt_in);
     lines += "launch " + k.name + " " + std::to_string(grid.x) + " " + std::to_string(block.x) + " " +
              std::to_string(shared) + " " + std::to_string(cluster) + (fits ? " ok\n" : " refused\n");
     if (fits && !fails("launch"))
