@@ -614,7 +614,9 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.max_kv = max_kv_tokens;
     const int chunks = pr.dn / kChunk;
     const size_t smem = (size_t)(chunks + stages_of(chunks)) * kBox + kOutBytes + sizeof(Bars);
-    if (cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // the opt-in is the kernel's, not the call's: the same for every width, so
+    // that no call lowers it under another one's launch
+    if (cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     const long long units = (cap + 1) / 2 * pr.NU * pairs, most = sm_count() / 2;
     cudaLaunchConfig_t cfg{};

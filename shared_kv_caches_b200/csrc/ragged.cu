@@ -85,8 +85,10 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st)
 {
     const size_t smem = (size_t)(a.batch + 1) * sizeof(int32_t);
     if (smem > 40 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // for the largest batch: the opt-in is the kernel's, and calls at the
+        // same time share it
+        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)((kMaxBatch + 1) * sizeof(int32_t)));
         if (e != cudaSuccess)
             return e;
     }

@@ -38,6 +38,9 @@ struct TableArgs {
     int32_t *table, *seq_lens, *free_left, *q_start, *kv_start, *pos, *slots, *err;
 };
 
+// Shared memory of the sums over the requests.
+constexpr size_t table_smem(int batch) { return (3 * (size_t)batch + 2) * sizeof(int32_t); }
+
 __device__ __forceinline__ int pages_of(long long n) { return (int)((n + kPage - 1) / kPage); }
 
 __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const TableArgs a)
@@ -382,11 +385,12 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
     const bool in_place = seq_lens == cached_lens || free_left == free_count;
     const int most = in_place ? kTableMaxCtas : sm_count();
     ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
-    const size_t smem = (3 * (size_t)batch + 2) * sizeof(int32_t);
+    const size_t smem = table_smem(batch);
     // the 48 KB of a launch without an opt-in hold what the kernel declares
-    // itself (272 bytes) too
+    // itself (272 bytes) too; the opt-in is for the largest batch, so that no
+    // call lowers it under another one's launch
     if (smem > 40 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess)
+                                                 (int)table_smem(ragged::kMaxBatch)) != cudaSuccess)
         return KVATTN_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);

@@ -89,3 +89,45 @@ def test_tables_of_any_batch_fit_their_shared_memory(rt, batch):
     first call near the 48 KB of a launch without an opt-in goes through."""
     assert tables(batch) == 0
     assert rt.launches("build_tables_kernel")[-1]["shared"] == 12 * batch + 8
+
+
+# ------------------------------------- opt-ins that calls at once may share
+
+def sizes_asked(rt, kernel):
+    """The opt-ins of a kernel and the shared memory of its launches.  An
+    opt-in is the kernel's, on its device, for every host thread: were it one
+    call's own, another call could lower it before this one's launch."""
+    return set(rt.opt_ins(kernel)), {x["shared"] for x in rt.launches(kernel)}
+
+
+def check_sizes(rt, kernel):
+    opt_ins, shared = sizes_asked(rt, kernel)
+    assert len(shared) > 1 and len(opt_ins) == 1 and max(shared) <= max(opt_ins)
+
+
+def expand(d_c, batch=2, n=50000):
+    p = K.make_params(batch, 16, 1, d_c, 64, 4, 9, 0)
+    return K.kvattn_expand_kv(K.KVATTN_MLA, p, FAKE, FAKE, FAKE, n, 128, 128, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None, None)
+
+
+def prefill(batch=2, n=50000, d=128):
+    p = K.kvattn_prefill_params(batch, 8, 8, d, 0, 128, n, n, 1, 0, 0)
+    return K.kvattn_prefill(p, FAKE, None, FAKE, None, FAKE, FAKE, FAKE, 0.1, FAKE, None, FAKE, 1 << 40, None, None)
+
+
+def test_one_opt_in_for_tables_of_every_size(rt):
+    for batch in (16384, 5000, 10000):
+        assert tables(batch) == 0
+    check_sizes(rt, "build_tables_kernel")
+
+
+def test_one_opt_in_for_expansions_of_every_width(rt):
+    for d_c in (512, 64, 256, 128):
+        assert expand(d_c) == 0
+    check_sizes(rt, "expand_kernel")
+
+
+def test_one_opt_in_for_lists_of_every_length(rt):
+    for batch in (16384, 12000, 11000):
+        assert expand(128, batch) == 0 and prefill(batch) == 0
+    check_sizes(rt, "plan_kernel")

@@ -837,3 +837,39 @@ def test_tables_first_call_of_a_process(dev, batch):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FRESH, str(batch)], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_of_several_host_threads(dev):
+    """Expansions of two widths and tables of two batches at once, each thread with its own stream and buffers."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(27)
+    jobs = []
+    for dc, batch in ((512, 9000), (64, 5000)):
+        cache, table, uk, uv, p, mpps = expand_case(rng, dev, 2, 1, dc, 16, 64, 64, [100, 70])
+        x = [up(cache, dev), i32(table, dev), i32(starts([100, 70]), dev), up(uk, dev), up(uv, dev)]
+        one = i32([1] * batch, dev)
+        pool = i32(np.arange(batch), dev)
+        jobs.append((p, x, one, one * 0, pool, i32([batch], dev), i32(np.full((batch, 1), -1), dev), batch))
+    torch.cuda.synchronize()
+    want = [K.expand_kv_tensors(K.KVATTN_MLA, j[0], *j[1], 170)["k"].clone() for j in jobs]
+    torch.cuda.synchronize()
+    faults = []
+
+    def work(j, ref):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(300):
+                    got = K.expand_kv_tensors(K.KVATTN_MLA, j[0], *j[1], 170)
+                    t = K.build_tables_tensors(j[3], j[2], j[4], j[5], j[6], j[7])
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(got["k"], ref) and int(t["free_left"]) == 0
+        except Exception as e:          # a thread's failure is the test's
+            faults.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not faults, faults
