@@ -163,9 +163,13 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a)
 template <int PRE>
 cudaError_t launch_combine_pre(const CombineArgs &a, size_t smem, cudaStream_t st)
 {
-    if (smem > 48 * 1024) {
+    // what the kernel declares counts against the 48 KB of a launch without an
+    // opt-in; the opt-in is all that is left beside it, for every call the
+    // same (it is the kernel's, and calls at the same time share it)
+    constexpr size_t declared = kMaxV4 * sizeof(float4);
+    if (smem + declared > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(combine_kernel<PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+                                             (int)(227 * 1024 - declared));
         if (e != cudaSuccess)
             return e;
     }

@@ -244,8 +244,10 @@ __global__ void __launch_bounds__(kThreads) generic_decode_kernel(const DecodeAr
 template <int HC>
 cudaError_t launch_hc(const DecodeArgs &a, size_t smem, cudaStream_t st)
 {
+    // all that a block may have, for every shape the same: the opt-in is the
+    // kernel's, and calls at the same time share it
     cudaError_t e = cudaFuncSetAttribute(generic_decode_kernel<HC>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess)
         return e;
     dim3 grid(a.num_splits, a.NU * a.head_chunks, a.B);

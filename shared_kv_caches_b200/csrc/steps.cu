@@ -298,8 +298,10 @@ cudaError_t launch_head_proj(const CUtensorMap &xm, const CUtensorMap &wm, void 
     const int chunks = k / kHpChunk;
     const int stages = chunks < kHpStages ? chunks : kHpStages;
     const size_t smem = HpLayout<NT>::bytes(stages);
-    cudaError_t e =
-        cudaFuncSetAttribute(head_proj_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // for the deepest ring: the opt-in is the kernel's, and calls at the same
+    // time share it
+    cudaError_t e = cudaFuncSetAttribute(head_proj_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)HpLayout<NT>::bytes(kHpStages));
     if (e != cudaSuccess)
         return e;
     const dim3 grid(heads, n / NT, (rows + 127) / 128);

@@ -131,3 +131,34 @@ def test_one_opt_in_for_lists_of_every_length(rt):
     for batch in (16384, 12000, 11000):
         assert expand(128, batch) == 0 and prefill(batch) == 0
     check_sizes(rt, "plan_kernel")
+
+
+def decode(variant, heads, kv, dn, dr, splits=0, pages=4096, batch=1):
+    p = K.make_params(batch, heads, kv, dn, dr, pages, pages * batch, pages * 64, splits)
+    return K.kvattn_decode(variant, p, FAKE, FAKE if dr else None, FAKE, FAKE, FAKE, 0.1, FAKE, None, FAKE, K.kvattn_workspace_size(variant, p), None)
+
+
+def test_one_opt_in_for_generic_decodes_of_every_width(rt):
+    for dn, dr in ((512, 128), (264, 8), (64, 0)):
+        assert decode(K.KVATTN_MLA, 3, 1, dn, dr) == 0
+    check_sizes(rt, "generic_decode_kernel")
+
+
+def test_one_opt_in_for_merges_of_every_number_of_parts(rt):
+    for branches in (48, 16, 13):
+        assert decode(K.KVATTN_MLRA, branches, branches, 64, 8, splits=1024) == 0
+    check_sizes(rt, "combine_kernel")
+
+
+def test_merges_near_48_kb_go_through(rt):
+    """The merge declares 2 KB of its own."""
+    rt.lib.fake_fixed(b"combine_kernel", 2048)
+    assert decode(K.KVATTN_MLRA, 12, 12, 64, 8, splits=1024) == 0
+    assert rt.launches("combine_kernel")[-1]["shared"] == 48 * 1024
+
+
+def test_one_opt_in_for_projections_of_every_depth(rt):
+    for k in (512, 64, 128):
+        assert K.kvattn_head_proj(FAKE, FAKE, FAKE, 0, 4, 200, k, 64, None, None) == 0
+    for kernel in {r[1] for r in rt.lines("launch", "head_proj_kernel")}:
+        check_sizes(rt, kernel)
