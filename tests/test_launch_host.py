@@ -140,20 +140,20 @@ def decode(variant, heads, kv, dn, dr, splits=0, pages=4096, batch=1):
 
 def test_one_opt_in_for_generic_decodes_of_every_width(rt):
     for dn, dr in ((512, 128), (264, 8), (64, 0)):
-        assert decode(K.KVATTN_MLA, 3, 1, dn, dr) == 0
+        assert decode(K.KVATTN_MLA, 4, 1, dn, dr) == 0
     check_sizes(rt, "generic_decode_kernel")
 
 
 def test_one_opt_in_for_merges_of_every_number_of_parts(rt):
-    for branches in (48, 16, 13):
-        assert decode(K.KVATTN_MLRA, branches, branches, 64, 8, splits=1024) == 0
+    for branches in (16, 13, 14):
+        assert decode(K.KVATTN_MLRA, 16, branches, 64, 8, splits=1024) == 0
     check_sizes(rt, "combine_kernel")
 
 
 def test_merges_near_48_kb_go_through(rt):
     """The merge declares 2 KB of its own."""
     rt.lib.fake_fixed(b"combine_kernel", 2048)
-    assert decode(K.KVATTN_MLRA, 12, 12, 64, 8, splits=1024) == 0
+    assert decode(K.KVATTN_MLRA, 16, 12, 64, 8, splits=1024) == 0
     assert rt.launches("combine_kernel")[-1]["shared"] == 48 * 1024
 
 
