@@ -588,8 +588,9 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     pa.tiles = reinterpret_cast<ragged::Tile *>(ws + ragged::kPlanHeader);
     pa.err = device_error;
     const bool listed = !ragged::small_plan(pa.batch, cap);
-    if (listed && ragged::launch_plan(pa, s) != cudaSuccess)
-        return KVATTN_ERR_CUDA;
+    cudaError_t e = listed ? ragged::launch_plan(pa, s) : cudaSuccess;
+    if (e != cudaSuccess)
+        return launch_status(e);
     ExpandArgs a{};
     a.plan = pa;
     a.listed = listed;
@@ -616,8 +617,9 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     const size_t smem = (size_t)(chunks + stages_of(chunks)) * kBox + kOutBytes + sizeof(Bars);
     // the opt-in is the kernel's, not the call's: the same for every width, so
     // that no call lowers it under another one's launch
-    if (cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
-        return KVATTN_ERR_CUDA;
+    e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess)
+        return launch_status(e);
     const long long units = (cap + 1) / 2 * pr.NU * pairs, most = sm_count() / 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * (units < most ? units : most)));
@@ -629,6 +631,5 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = listed ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, expand_kernel, cm, km, vm, ko, vo, (const ExpandArgs)a) == cudaSuccess ? KVATTN_OK
-                                                                                                   : KVATTN_ERR_CUDA;
+    return launch_status(cudaLaunchKernelEx(&cfg, expand_kernel, cm, km, vm, ko, vo, (const ExpandArgs)a));
 }

@@ -182,6 +182,17 @@ __device__ __forceinline__ bool finish_part(const DecodeArgs &a, int ticket_idx,
 // through the runtime; kDefaultSMs when there is no device).
 int sm_count();
 
+// Status of a call that e ends.  The runtime keeps a failure as its last error
+// until it is asked for: it is taken off here, or the next call that checks its
+// launch would report it as its own.
+inline int launch_status(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return KVATTN_OK;
+    cudaGetLastError();
+    return KVATTN_ERR_CUDA;
+}
+
 // Argument checks shared by every decode entry point: the problem, the
 // pointers and their alignment, sm_scale.  Returns a kvattn_status; nothing
 // is enqueued.

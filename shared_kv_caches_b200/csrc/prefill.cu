@@ -991,8 +991,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     c.stream = static_cast<cudaStream_t>(stream);
     c.most_items = pa.capacity * H;
     const bool listed = needs_plan(p);
-    if (listed && ragged::launch_plan(pa, c.stream) != cudaSuccess)
-        return KVATTN_ERR_CUDA;
+    cudaError_t e = listed ? ragged::launch_plan(pa, c.stream) : cudaSuccess;
+    if (e != cudaSuccess)
+        return launch_status(e);
     PrefillArgs &a = c.args;
     a.plan = pa;
     a.listed = listed;
@@ -1019,12 +1020,11 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
 
     const int nkn = (p->d_nope + 63) / 64, nvb = (p->d_v + 63) / 64;
     const bool rope = p->d_rope > 0;
-    cudaError_t e;
     if (nvb == 2)
         e = nkn == 2 ? (rope ? launch<3, true, 2>(c) : launch<2, false, 2>(c))
                      : (rope ? launch<2, true, 2>(c) : launch<1, false, 2>(c));
     else
         e = nkn == 2 ? (rope ? launch<3, true, 1>(c) : launch<2, false, 1>(c))
                      : (rope ? launch<2, true, 1>(c) : launch<1, false, 1>(c));
-    return e == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
+    return launch_status(e);
 }

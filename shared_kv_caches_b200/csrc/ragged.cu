@@ -92,8 +92,13 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st)
         if (e != cudaSuccess)
             return e;
     }
-    plan_kernel<<<1, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    // (launched so that the status is this launch's, not an earlier call's)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, plan_kernel, a);
 }
 
 }  // namespace ragged

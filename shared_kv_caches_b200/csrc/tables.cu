@@ -389,9 +389,12 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
     // the 48 KB of a launch without an opt-in hold what the kernel declares
     // itself (272 bytes) too; the opt-in is for the largest batch, so that no
     // call lowers it under another one's launch
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)table_smem(ragged::kMaxBatch)) != cudaSuccess)
-        return KVATTN_ERR_CUDA;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)table_smem(ragged::kMaxBatch));
+        if (e != cudaSuccess)
+            return launch_status(e);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTableThreads);
@@ -404,7 +407,7 @@ extern "C" int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = in_place && ctas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, build_tables_kernel, (const TableArgs)a) == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
+    return launch_status(cudaLaunchKernelEx(&cfg, build_tables_kernel, (const TableArgs)a));
 }
 
 extern "C" int kvattn_append_slots(int32_t variant, const kvattn_params *p, const void *new_kv, int32_t num_tokens,
@@ -454,10 +457,11 @@ extern "C" int kvattn_append_slots(int32_t variant, const kvattn_params *p, cons
     const long long want = ((long long)num_tokens + per - 1) / per;
     const long long most = 4LL * sm_count();      // the blocks that are resident: rates are formed once a warp
     const int grid = (int)(want < most ? want : most);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fp8)
-        append_slots_kernel<true><<<grid, kAppendThreads, 0, s>>>(a);
-    else
-        append_slots_kernel<false><<<grid, kAppendThreads, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? KVATTN_OK : KVATTN_ERR_CUDA;
+    // (launched so that the status is this launch's, not an earlier call's)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kAppendThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    return launch_status(cudaLaunchKernelEx(&cfg, fp8 ? append_slots_kernel<true> : append_slots_kernel<false>,
+                                            (const SlotAppendArgs)a));
 }

@@ -162,3 +162,29 @@ def test_one_opt_in_for_projections_of_every_depth(rt):
         assert K.kvattn_head_proj(FAKE, FAKE, FAKE, 0, 4, 200, k, 64, None, None) == 0
     for kernel in {r[1] for r in rt.lines("launch", "head_proj_kernel")}:
         check_sizes(rt, kernel)
+
+
+# ------------------------------------------------ errors of calls before
+
+def append(n=4):
+    p = K.make_params(1, 16, 1, 512, 64, 4, 9, 0)
+    return K.kvattn_append_slots(K.KVATTN_MLA, p, FAKE, n, FAKE, FAKE, FAKE, 1e4, None, None)
+
+
+@pytest.mark.parametrize("call", [append, lambda: expand(512), prefill, lambda: tables(4)],
+                         ids=["append", "expand", "prefill", "tables"])
+def test_an_error_left_by_another_call_is_not_this_ones(rt, call):
+    """The runtime keeps the last error until someone asks for it: a launch's
+    own status counts, not what an earlier call of the process left."""
+    rt.lib.fake_last_error(1)
+    assert call() == 0
+
+
+@pytest.mark.parametrize("where", ["cudaFuncSetAttribute", "launch"])
+@pytest.mark.parametrize("call", [append, lambda: expand(512), prefill, lambda: tables(16384)],
+                         ids=["append", "expand", "prefill", "tables"])
+def test_a_failed_call_takes_its_error_with_it(rt, call, where):
+    rt.lib.fake_fail(where.encode(), 1)
+    st = call()
+    assert st == (0 if call is append and where != "launch" else K.KVATTN_ERR_CUDA)
+    assert rt.lib.fake_peek() == 0
