@@ -53,6 +53,8 @@
 // 313; 24 heads or more gain there and lose on longer prompts).
 #include <math.h>
 
+#include <atomic>
+
 #include "latent_common.cuh"
 #include "ragged.cuh"
 
@@ -835,12 +837,16 @@ cudaError_t launch(const Call &c)
     if (e != cudaSuccess)
         return e;
     // the register split waits for good if the kernel is launched with fewer
-    static const int regs = [](const void *f) {
+    static std::atomic<bool> checked{false};
+    if (!checked.load(std::memory_order_relaxed)) {
         cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, f) == cudaSuccess ? at.numRegs : 0;
-    }(reinterpret_cast<const void *>(kern));
-    if (regs != kLaunchRegs)
-        return cudaErrorInvalidConfiguration;
+        const cudaError_t q = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(kern));
+        if (q != cudaSuccess)
+            return q;                        // asked again by the next call
+        if (at.numRegs != kLaunchRegs)
+            return cudaErrorInvalidConfiguration;
+        checked.store(true, std::memory_order_relaxed);
+    }
     const long long most = c.args.listed ? sm_count() : c.most_items;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c.most_items < most ? c.most_items : most));

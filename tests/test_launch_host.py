@@ -188,3 +188,11 @@ def test_a_failed_call_takes_its_error_with_it(rt, call, where):
     st = call()
     assert st == (0 if call is append and where != "launch" else K.KVATTN_ERR_CUDA)
     assert rt.lib.fake_peek() == 0
+
+
+# -------------------------------------------------------- calls that fail once
+
+def test_prefill_asks_again_where_its_registers_could_not_be_read(rt):
+    rt.lib.fake_fail(b"cudaFuncGetAttributes", 1)
+    assert prefill() == K.KVATTN_ERR_CUDA and not rt.launches("prefill_kernel")
+    assert prefill() == 0 and len(rt.launches("prefill_kernel")) == 1
