@@ -196,3 +196,9 @@ def test_prefill_asks_again_where_its_registers_could_not_be_read(rt):
     rt.lib.fake_fail(b"cudaFuncGetAttributes", 1)
     assert prefill() == K.KVATTN_ERR_CUDA and not rt.launches("prefill_kernel")
     assert prefill() == 0 and len(rt.launches("prefill_kernel")) == 1
+
+
+def test_tensor_maps_are_asked_for_again_where_the_driver_did_not_answer(rt):
+    rt.lib.fake_fail(b"cudaGetDriverEntryPoint", 1)
+    assert prefill() != 0 and not rt.launches("prefill_kernel") and rt.lib.fake_peek() == 0
+    assert prefill() == 0 and len(rt.launches("prefill_kernel")) == 1
