@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
 {
     extern __shared__ int32_t sh_i[];
     __shared__ long long sh_scan[32];
-    __shared__ int sh_taken;
+    __shared__ int sh_taken, sh_served;
     int32_t *tok = sh_i;                            // [B + 1] first token of each chunk (at most max_tokens)
     int32_t *pgs = sh_i + a.batch + 1;              // [B + 1] new pages of the requests before
     int32_t *cch = sh_i + 2 * (a.batch + 1);        // [B] cached tokens, or -1 - cached where the request gets nothing
@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
     npg = ragged::block_scan(npg, pg_total, sh_scan);
     long long ctx = 0, ctx_total;
     int taken = 0;
+    bool late = false;                              // requests here that want pages, but whose tokens do not fit
     {
         long long t = ntok, p = npg;
         for (int b = b0; b < b1; ++b) {
@@ -100,8 +101,10 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
             if (n > 0 && t > a.max_tokens) {
                 bits |= KVATTN_DEVERR_TOO_MANY_TOKENS;
                 ok = false;
-            }
-            if (pages > 0 && p > nfree) {
+                late |= pages > 0;
+                if (t - n <= a.max_tokens)          // the first of them
+                    sh_served = (int)min(p - pages, (long long)INT32_MAX);
+            } else if (pages > 0 && p > nfree) {
                 bits |= KVATTN_DEVERR_POOL_EXHAUSTED;
                 ok = false;
             }
@@ -120,6 +123,19 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
         sh_taken = 0;
     }
     ctx = ragged::block_scan(ctx, ctx_total, sh_scan);
+    // a request whose tokens do not fit takes no pages: the list is too short
+    // for it only where it lacks pages beside those of the requests before
+    // the first such one
+    if (late) {
+        long long t = ntok;
+        for (int b = b0; b < b1; ++b) {
+            int c, n, pages;
+            request(b, c, n, pages);
+            t += n;
+            if (n > 0 && t > a.max_tokens && pages > 0 && (long long)sh_served + pages > nfree)
+                bits |= KVATTN_DEVERR_POOL_EXHAUSTED;
+        }
+    }
     if (taken > 0)
         atomicMax(&sh_taken, taken);
     if (rank == 0 && bits && a.err)

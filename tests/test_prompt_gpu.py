@@ -873,3 +873,39 @@ def test_calls_of_several_host_threads(dev):
     for t in threads:
         t.join()
     assert not faults, faults
+
+
+# ------------------------------------- what the tables say of refused requests
+
+@pytest.mark.parametrize("new,tokens,pages,want", [
+    ([64] * 5, 64, 3, prompt.ERR_TOKENS),                       # one page taken, two left: only the tokens ran out
+    ([64, 640], 64, 3, prompt.ERR_TOKENS | prompt.ERR_POOL),    # ten pages wanted of two
+    ([64, 64, 64], 128, 1, prompt.ERR_TOKENS | prompt.ERR_POOL),
+    ([64, 128, 0, 64], 64, 3, prompt.ERR_TOKENS),
+    ([1] * 3000, 70, 2980, prompt.ERR_TOKENS),
+])
+def test_tables_refused_for_tokens_do_not_use_up_the_pool(dev, new, tokens, pages, want):
+    rng = np.random.default_rng(28)
+    cached, free = np.zeros(len(new), int), rng.permutation(pages)
+    table = np.full((len(new), 10), -7)
+    ref = prompt.build_tables(cached, new, free, pages, table, tokens, pages)
+    assert ref["err"] == want
+    same_tables(run_tables(dev, cached, new, table, free, pages, tokens), ref)
+
+
+def test_tables_error_words_of_random_requests(dev):
+    """Tokens, pages and table rows that run out at different requests."""
+    rng = np.random.default_rng(29)
+    seen = set()
+    for _ in range(60):
+        n = int(rng.integers(1, 40))
+        cached, new = rng.integers(0, 150, n), rng.integers(0, 200, n) * (rng.random(n) < 0.8)
+        table, free, count, pages = table_case(rng, cached, new, shrink=int(rng.integers(0, 40)) * int(rng.random() < 0.6))
+        if rng.random() < 0.3:
+            table = table[:, :max(table.shape[1] - 1, 1)]
+            cached = np.minimum(cached, 64 * table.shape[1])
+        m = max(int(new.sum()) + 5 - int(rng.integers(0, 600)) * int(rng.random() < 0.6), 0)
+        ref = prompt.build_tables(cached, new, free, count, table, m, pages)
+        seen.add(ref["err"])
+        same_tables(run_tables(dev, cached, new, table, free, count, m), ref)
+    assert {0, prompt.ERR_TOKENS, prompt.ERR_POOL, prompt.ERR_TOKENS | prompt.ERR_POOL} <= seen
