@@ -412,7 +412,7 @@ int kvattn_head_proj(const void *x, const void *w, void *y, int32_t out_dtype, i
  *
  * A request that cannot be served gets no pages, slots of -1 and its cached
  * length, and its error bit is set: SEQ_TOO_LONG past max_pages_per_seq * 64
- * tokens, POOL_EXHAUSTED where the free list ends (for it and for every later
+ * or 2^31 - 1 tokens, POOL_EXHAUSTED where the free list ends (for it and for every later
  * request that needs a page), TOO_MANY_TOKENS likewise where max_tokens ends
  * (q_start stops there), BAD_LENGTH for a negative length (taken as 0).
  * PAGE_OUT_OF_RANGE: a page id outside [0, num_pages), in the table or the free

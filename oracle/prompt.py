@@ -33,7 +33,7 @@ def build_tables(cached, new, free_pages, free_count, block_table, max_tokens, n
         if c < 0 or n < 0:
             err |= ERR_LENGTH
             c, n, ok = max(c, 0), max(n, 0), False
-        elif c + n > mpps * PAGE:
+        elif c + n > min(mpps * PAGE, 2 ** 31 - 1):
             err |= ERR_LONG
             ok = False
         held, need = -(-c // PAGE), -(-(c + n) // PAGE)

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) build_tables_kernel(const Ta
     int32_t *pgs = sh_i + a.batch + 1;              // [B + 1] new pages of the requests before
     int32_t *cch = sh_i + 2 * (a.batch + 1);        // [B] cached tokens, or -1 - cached where the request gets nothing
     const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
-    const long long capacity = (long long)a.mpps * kPage;
+    const long long capacity = min((long long)a.mpps * kPage, (long long)INT32_MAX);   // lengths are 32-bit numbers
     const int raw_free = *a.free_count;
     const int nfree = min(max(raw_free, 0), a.num_pages);
     int bits = raw_free == nfree ? 0 : KVATTN_DEVERR_BAD_LENGTH;

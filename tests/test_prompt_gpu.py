@@ -909,3 +909,18 @@ def test_tables_error_words_of_random_requests(dev):
         seen.add(ref["err"])
         same_tables(run_tables(dev, cached, new, table, free, count, m), ref)
     assert {0, prompt.ERR_TOKENS, prompt.ERR_POOL, prompt.ERR_TOKENS | prompt.ERR_POOL} <= seen
+
+
+@pytest.mark.parametrize("new", [9, 10, 11])
+def test_tables_lengths_end_at_31_bits(dev, new):
+    """A table with room for 2^31 tokens: a length of 2^31 - 1 is served, the next one is refused."""
+    import torch
+    table = torch.zeros(1, 1 << 25, dtype=torch.int32, device=dev)
+    err = word(dev)
+    r = K.build_tables_tensors(i32([2 ** 31 - 10], dev), i32([new], dev), i32(np.arange(9), dev), i32([0], dev), table, 16,
+                               device_error=err)
+    fits = new == 9
+    assert int(err.item()) == (0 if fits else K.KVATTN_DEVERR_SEQ_TOO_LONG)
+    assert int(r["seq_lens"]) == 2 ** 31 - 10 + (9 if fits else 0) and int(r["kv_start"][1]) == int(r["seq_lens"])
+    want = [(2 ** 31 - 10 + i) % 64 for i in range(9)] if fits else [-1] * new
+    assert r["slots"].tolist()[:len(want)] == want and r["slots"].tolist()[new:] == [-1] * (16 - new)
