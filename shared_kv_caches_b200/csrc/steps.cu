@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include "kvattn_internal.cuh"
+#include "rope.cuh"
 #include "sm100.cuh"
 
 namespace kvattn {
@@ -37,13 +38,12 @@ bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 // Turn the pair (x0, x1), pair index i of a d-wide slice, at position pos.
 __device__ __forceinline__ __nv_bfloat162 rope_pair(__nv_bfloat162 v, long long pos, int i, int d, double log2_base)
 {
-    const double inv_freq = exp2(-2.0 * (double)i / (double)d * log2_base);
-    double s, c;
-    sincos((double)pos * inv_freq, &s, &c);
-    const double x0 = (double)__bfloat162float(v.x), x1 = (double)__bfloat162float(v.y);
+    double s, c, r0, r1;
+    rope_angle(pos, rope_rate(i, d, log2_base), &s, &c);
+    rope_turn((double)__bfloat162float(v.x), (double)__bfloat162float(v.y), s, c, &r0, &r1);
     __nv_bfloat162 r;
-    r.x = __double2bfloat16(x0 * c - x1 * s);
-    r.y = __double2bfloat16(x0 * s + x1 * c);
+    r.x = __double2bfloat16(r0);
+    r.y = __double2bfloat16(r1);
     return r;
 }
 

@@ -20,6 +20,7 @@
 #include <math.h>
 
 #include "ragged.cuh"
+#include "rope.cuh"
 
 namespace kvattn {
 
@@ -233,12 +234,6 @@ struct SlotAppendArgs {
     float k_scale, v_scale;       // fp8: what a stored value is multiplied by when it is read
 };
 
-// Turns (of pi) that pair i of a width-wide slice makes per position.
-__device__ __forceinline__ double rope_rate(int i, int width, double log2_base)
-{
-    return exp2(-2.0 * (double)i / (double)width * log2_base) * 0.31830988618379067;
-}
-
 // x / scale in fp32; exactly the product with 1 / scale where that is a power of two.
 __device__ __forceinline__ float unscaled(float x, float scale, float inverse, bool exact)
 {
@@ -275,11 +270,11 @@ constexpr int kAppendHeads = 8;
 // One warp per token: 16-byte copies of what is stored as it is; a turned
 // pair belongs to one lane, which forms its angle once for the token and turns
 // the pair of every slice (every K head) with it.  The angle and the turn are
-// in double precision with one rounding to the stored type, as kvattn_rope's
-// (in turns of pi: the whole turns of a far position come off exactly); a lane's first two rates (all it has for slices up to 128 wide) stay in
-// registers over its tokens.  Bound by memory latency: a row's loads do not
-// wait for its slot or for the angles, which are formed while they are under
-// way.
+// in double precision with one rounding to the stored type, by the routine that
+// kvattn_rope uses; a lane's first two rates (all it has for slices up to 128
+// wide) stay in registers over its tokens.  Bound by memory latency: a row's
+// loads do not wait for its slot or for the angles, which are formed while they
+// are under way.
 template <bool FP8>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_slots_kernel(const SlotAppendArgs a)
 {
@@ -336,14 +331,14 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_slots_kernel(const S
                         if (n0 + n < a.rot_count)
                             v[n] = *reinterpret_cast<const __nv_bfloat162 *>(src + copy + (n0 + n) * a.rot_width + 2 * i);
                     if (n0 == 0)
-                        sincospi((double)pos * rate, &s, &c);
+                        rope_angle(pos, rate, &s, &c);
 #pragma unroll
                     for (int n = 0; n < kAppendHeads; ++n) {
                         if (n0 + n >= a.rot_count)
                             break;
                         const int e = copy + (n0 + n) * a.rot_width + 2 * i;
-                        const double x = (double)__bfloat162float(v[n].x), y = (double)__bfloat162float(v[n].y);
-                        const double rx = x * c - y * s, ry = x * s + y * c;
+                        double rx, ry;
+                        rope_turn((double)__bfloat162float(v[n].x), (double)__bfloat162float(v[n].y), s, c, &rx, &ry);
                         if constexpr (FP8) {
                             // one rounding to e4m3 but for the one to fp32 in
                             // front of it, 20 bits finer

@@ -924,3 +924,53 @@ def test_tables_lengths_end_at_31_bits(dev, new):
     assert int(r["seq_lens"]) == 2 ** 31 - 10 + (9 if fits else 0) and int(r["kv_start"][1]) == int(r["seq_lens"])
     want = [(2 ** 31 - 10 + i) % 64 for i in range(9)] if fits else [-1] * new
     assert r["slots"].tolist()[:len(want)] == want and r["slots"].tolist()[new:] == [-1] * (16 - new)
+
+
+# ------------------------------------------------------ one turn for all calls
+
+@pytest.mark.parametrize("top", [1 << 15, 1 << 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("variant,kv,dn,dr", [("mla", 1, 64, 64), ("gqa", 2, 128, 0)])
+def test_append_turns_exactly_as_rope_does(dev, top, variant, kv, dn, dr):
+    """Bit for bit, near and far: the rounding of a far angle reaches the stored bits where the two form it apart."""
+    import torch
+    rng = np.random.default_rng(30)
+    n = 30000
+    pages, base = -(-n // 64), W.ROPE_BASE
+    pos = i32(rng.integers(-(top // 8), top, n), dev)
+    slots = i32(rng.permutation(pages * 64)[:n], dev)
+    p = K.make_params(1, 2 * kv, kv, dn, dr, pages, pages, 0)
+    if dr:
+        rows = up(bits(rng, n, dn + dr), dev)
+        cache = torch.zeros(pages, 64, dn + dr, dtype=torch.bfloat16, device=dev)
+        K.append_slots_tensor(K.VARIANTS[variant], p, rows, pos, slots, cache, base)
+        got = cache.view(-1, dn + dr)[slots.long()]
+        K.rope_tensor(rows, pos, dn, dr, base, 1)
+    else:
+        rows = up(bits(rng, n, 2, kv * dn), dev)
+        cache = torch.zeros(pages, 2, 64, kv * dn, dtype=torch.bfloat16, device=dev)
+        K.append_slots_tensor(K.VARIANTS[variant], p, rows, pos, slots, cache, base)
+        got = cache.transpose(1, 2).reshape(-1, 2, kv * dn)[slots.long()]
+        keys = rows[:, 0].contiguous().view(n * kv, dn)
+        K.rope_tensor(keys, pos, 0, dn, base, kv)
+        rows[:, 0] = keys.view(n, kv * dn)
+    assert torch.equal(got.view(torch.int16), rows.view(torch.int16))
+
+
+def test_both_appends_store_the_same_bits(dev):
+    import torch
+    rng = np.random.default_rng(31)
+    B, Q, row, mpps = 40, 64, 576, 600
+    pages = B * Q
+    rows = up(bits(rng, B, Q, row), dev)
+    pos = np.array([rng.choice(mpps * 64, Q, replace=False) for _ in range(B)])
+    table = np.zeros((B, mpps), int)
+    for b in range(B):              # a page of its own for every page that a position falls in
+        table[b, pos[b] // 64] = b * Q + np.arange(Q)
+    slots = np.take_along_axis(table, pos // 64, 1) * 64 + pos % 64
+    p = K.make_params(B, 8, 1, 512, 64, mpps, pages, mpps * 64, q_len=Q)
+    one, two = (torch.zeros(pages, 64, row, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    t, ps, tab = i32(slots.reshape(-1), dev), i32(pos, dev), i32(table, dev)
+    assert K.kvattn_append_kv(K.KVATTN_MLA, p, rows.data_ptr(), ps.data_ptr(), tab.data_ptr(), one.data_ptr(), W.ROPE_BASE, None,
+                              torch.cuda.current_stream().cuda_stream) == 0
+    K.append_slots_tensor(K.KVATTN_MLA, p, rows.view(-1, row), ps.view(-1), t, two, W.ROPE_BASE)
+    assert torch.equal(one.view(torch.int16), two.view(torch.int16))
