@@ -730,9 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = row < it->nq;
             const int head = it->head;
             const long long grow = (long long)it->q0 + row;
-            // values that are not finite, of tokens near the rows' ends: rare
+            // values that are not finite, of tokens near the rows' ends: rare.
+            // The guard's notes are read of this query tile's own edge tiles
+            // alone: it was done with those before their P.V.  An item without
+            // one may be stored before the guard has taken it, and the other
+            // query tile's may still be written.
+            const int noted = n > 0 ? n - it->all / kKeys : 0;
             uint32_t any_bad = 0;
-            for (int e = lane; e < kEdgeTiles * (kKeys / 32); e += 32)
+            for (int e = lane; e < noted * (kKeys / 32); e += 32)
                 any_bad |= B.bad[taken % kItems][e / (kKeys / 32)][e % (kKeys / 32)];
             any_bad = __any_sync(0xffffffffu, any_bad != 0);
             const bool any = n > 0 && l != 0.f;          // a row without keys has l = 0 (NaN passes)
@@ -750,13 +755,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int y = 0; y < 64; ++y)
                     f[y] = any ? f[y] * inv : 0.f;
-                if (any_bad && n > 0) {
+                if (any_bad) {
                     // P.V took them as 0: the rows that attend their tokens get them here
                     const int edge = it->all / kKeys;
                     const __nv_bfloat16 *const v0 = a.v + (long long)it->k0 * a.v_token_stride +
                                                     (head / a.heads_per_kv) * a.v_head_stride + x;
 #pragma unroll 1
-                    for (int e = 0; e < kEdgeTiles * kKeys; ++e) {
+                    for (int e = 0; e < noted * kKeys; ++e) {
                         const int tok = edge * kKeys + e;
                         if (!(B.bad[taken % kItems][e / kKeys][e % kKeys / 32] >> (e % 32) & 1) || tok >= lim)
                             continue;
