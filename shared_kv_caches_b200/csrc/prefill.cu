@@ -1025,8 +1025,9 @@ extern "C" int kvattn_prefill(const kvattn_prefill_params *p, const void *q_nope
     a.v_token_stride = sv[0];
     a.v_head_stride = sv[1];
     // masked scores are infinite, so a scale of 0 (every key weighs the same)
-    // is taken as one too small to show in any weight
-    a.scale_log2 = sm_scale == 0.f ? 1e-30f : fabsf(sm_scale) * 1.4426950408889634f;
+    // is taken as the smallest there is: times any finite score it is below
+    // 2^-20, too small to show in a weight
+    a.scale_log2 = sm_scale == 0.f ? 1.4e-45f : fabsf(sm_scale) * 1.4426950408889634f;
     a.negate = sm_scale < 0.f ? 1u << 13 : 0u;
 
     const int nkn = (p->d_nope + 63) / 64, nvb = (p->d_v + 63) / 64;

@@ -974,3 +974,25 @@ def test_both_appends_store_the_same_bits(dev):
                               torch.cuda.current_stream().cuda_stream) == 0
     K.append_slots_tensor(K.KVATTN_MLA, p, rows.view(-1, row), ps.view(-1), t, two, W.ROPE_BASE)
     assert torch.equal(one.view(torch.int16), two.view(torch.int16))
+
+
+@pytest.mark.parametrize("reach", [1.0, 1e14, 1e18])
+def test_prefill_scale_zero_weighs_every_key_the_same(dev, reach):
+    """Whatever the scores are: below 2^127, so that the exponents stay below 2^-21.  A weight is 1 within 2^-21 and
+    rounds to 1 in bf16; 270 fp32 additions are off by 270 * 2^-24 < 2^-15 of sum |v|, those of the denominator by as
+    much: 2^-13 of the mean of |v| covers both, and the output's own rounding is 2^-8.  lse: 2^-15 of the denominator,
+    2^-21 of the maximum and the logarithm's own 2^-22."""
+    rng = np.random.default_rng(32)
+    ql, kl = [140], [270]
+    x = prefill_case(rng, 2, 2, 64, 0, 64, ql, kl)
+    x["q"][:140] = W.f32_to_bf16_bits((f64(x["q"][:140]) * reach).astype(np.float32))
+    x["k"][:, :270] = W.f32_to_bf16_bits((f64(x["k"][:, :270]) * reach).astype(np.float32))
+    got = call(dev, x, ql, kl, 0.0, True)
+    out, lse = down(got["out"])[:140], down(got["lse"])[:140]
+    for h in range(2):
+        v = f64(x["v"][h, :270])
+        for i in range(140):
+            n = i + 131
+            want, mass = v[:n].mean(0), np.abs(v[:n]).mean(0)
+            assert np.all(np.abs(out[i, h] - want) <= BF16 * np.abs(want) + 2.0 ** -13 * mass)
+            assert abs(lse[i, h] - np.log(n)) <= 2.0 ** -14
