@@ -996,3 +996,126 @@ def test_prefill_scale_zero_weighs_every_key_the_same(dev, reach):
             want, mass = v[:n].mean(0), np.abs(v[:n]).mean(0)
             assert np.all(np.abs(out[i, h] - want) <= BF16 * np.abs(want) + 2.0 ** -13 * mass)
             assert abs(lse[i, h] - np.log(n)) <= 2.0 ** -14
+
+
+# --------------------------------------------------- larger grids, first calls
+
+@pytest.mark.parametrize("tokens", [4097, 20000, 40000])
+def test_tables_in_place_with_many_tokens(dev, tokens):
+    """Lengths and free count updated in place while other CTAs read them (a cluster from 4097 tokens on, and more
+    tokens than its eight CTAs take at once): eager, then replayed in a graph."""
+    import torch
+    rng = np.random.default_rng(tokens)
+    B = 37
+    cached = rng.integers(0, 300, B)
+    new = rng.multinomial(tokens - 3, np.full(B, 1 / B))
+    steps = 4
+    table, free, count, pages = table_case(rng, cached, steps * new, mpps=int(-(-(cached + steps * new).max() // 64)) + 1)
+    lens, cnt, tab, one, pool = i32(cached, dev), i32([count], dev), i32(table, dev), i32(new, dev), i32(free, dev)
+    err = word(dev)
+    ref_c, ref_t, ref_n = cached, table, count
+
+    def same(r):
+        nonlocal ref_c, ref_t, ref_n
+        torch.cuda.synchronize()
+        ref = prompt.build_tables(ref_c, new, free, ref_n, ref_t, tokens, pages)
+        assert ref.pop("err") == 0 == int(err.item())
+        same_tables({k: v.cpu().numpy() for k, v in r.items()}, ref)
+        ref_c, ref_t, ref_n = ref["seq_lens"], ref["block_table"], int(ref["free_left"][0])
+
+    same(K.build_tables_tensors(lens, one, pool, cnt, tab, tokens, err, inplace=True))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = K.build_tables_tensors(lens, one, pool, cnt, tab, tokens, err, inplace=True)
+    for _ in range(steps - 1):
+        g.replay()
+        same(r)
+
+
+@pytest.mark.parametrize("H,G,dc,variant", [(20, 2, 64, "gla"), (14, 2, 128, "gla"), (5, 3, 64, "mlra"), (9, 1, 64, "mla")])
+def test_expand_more_tile_pairs_than_clusters(dev, H, G, dc, variant):
+    """Clusters that take whole tile pairs through every group and head pair, then runs of what is left."""
+    import torch
+    rng = np.random.default_rng(H)
+    lens = [9000, 1, 0, 7000, 130, 129] + [64] * 40
+    R = G if variant == "mlra" else 1
+    cache, table, _, _, p, mpps = expand_case(rng, dev, H, G, dc, 16, 16, 24, lens)
+    uk, uv = bits(rng, H, 16, R * dc, scale=dc ** -0.5), bits(rng, H, R * dc, 24, scale=dc ** -0.5)
+    err = word(dev)
+    x = (K.VARIANTS[variant], p, up(cache, dev), i32(table, dev), i32(starts(lens), dev), up(uk, dev), up(uv, dev), sum(lens), err)
+    got = K.expand_kv_tensors(*x)
+    assert int(err.item()) == 0
+    again = K.expand_kv_tensors(*x)
+    assert all(torch.equal(got[k].view(torch.int16), again[k].view(torch.int16)) for k in got)
+    if R == 1:
+        check_expand(got, cache, table, uk, uv, G, lens, mpps)
+        return
+    for r in range(R):
+        cols = np.r_[r * dc:(r + 1) * dc, R * dc:R * dc + 16]
+        one = dict(k=got["k"][r::R], v=got["v"][r::R], k_rope=got["k_rope"])
+        check_expand(one, cache[..., cols], table, uk[..., r * dc:(r + 1) * dc], uv[:, r * dc:(r + 1) * dc], 1, lens, mpps)
+
+
+CAPTURED = """
+import numpy as np, torch
+from shared_kv_caches_b200 import kvattn as K
+dev = "cuda:0"
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+gen = torch.Generator(dev).manual_seed(0)
+draw = lambda *s: torch.randn(*s, generator=gen, device=dev).to(torch.bfloat16)
+T, H, pages = {tokens}, 4, {tokens} // 64 + 2
+lens, new, pool, cnt, tab = i32([0, 0]), i32([T - 70, 70]), i32(np.arange(pages)), i32([pages]), i32(np.zeros((2, pages)))
+rows, q, qr, uk, uv = draw(T, 80), draw(T, H, 64), draw(T, H, 16), draw(H, 64, 64), draw(H, 64, 64)
+cache, err = torch.zeros(pages, 64, 80, dtype=torch.bfloat16, device=dev), i32([0])
+p = K.make_params(2, H, 1, 64, 16, pages, pages, 0)
+
+def step():
+    t = K.build_tables_tensors(lens, new, pool, cnt, tab, T, err)
+    K.append_slots_tensor(K.KVATTN_MLA, p, rows, t["pos"], t["slots"], cache, 1e4, err)
+    e = K.expand_kv_tensors(K.KVATTN_MLA, p, cache, tab, t["kv_start"], uk, uv, T, err)
+    return K.prefill_tensors(q, qr, e["k"], e["k_rope"], e["v"], t["q_start"], t["kv_start"], 0.1, device_error=err)
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+for _ in range(3):
+    g.replay()
+torch.cuda.synchronize()
+want = step()
+assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"]) and int(err) == 0
+assert bool(torch.isfinite(got["out"]).all()) and float(got["out"].float().abs().max()) > 0
+"""
+
+
+@pytest.mark.parametrize("tokens", [300, 9000])
+def test_a_process_whose_first_calls_are_captured(dev, tokens):
+    """A whole step captured before any call ran eagerly, with and without the plan's launch."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURED.format(tokens=tokens)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_expand_and_append_at_once_on_two_streams(dev):
+    """Expansions of the same cache on two streams with their own workspaces, beside appends to other pages."""
+    import torch
+    rng = np.random.default_rng(33)
+    lens = [3000, 200]
+    cache, table, uk, uv, p, mpps = expand_case(rng, dev, 4, 1, 128, 32, 64, 64, lens)
+    free = np.setdiff1d(np.arange(cache.shape[0]), table)[0]
+    x = (K.KVATTN_MLA, p, up(cache, dev), i32(table, dev), i32(starts(lens), dev), up(uk, dev), up(uv, dev), sum(lens))
+    rows, pos, slots = up(bits(rng, 64, 160), dev), i32(np.arange(64), dev), i32(free * 64 + np.arange(64), dev)
+    one = K.expand_kv_tensors(*x)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+            with torch.cuda.stream(s):
+                got.append(K.expand_kv_tensors(*x))
+        K.append_slots_tensor(K.KVATTN_MLA, p, rows, pos, slots, x[2], W.ROPE_BASE)
+    torch.cuda.synchronize()
+    for y in got:
+        assert all(torch.equal(one[k].view(torch.int16), y[k].view(torch.int16)) for k in one)
