@@ -279,7 +279,7 @@ template <bool FP8>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_slots_kernel(const SlotAppendArgs a)
 {
     const int lane = threadIdx.x & 31;
-    const int warps = gridDim.x * (kAppendThreads / 32);
+    const unsigned warps = gridDim.x * (kAppendThreads / 32);
     const int half = a.rot_width / 2;
     double rate0 = 0.0, rate1 = 0.0;
     if (a.rot_count > 0) {
@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_slots_kernel(const S
         if (half > 32)
             rate1 = rope_rate(lane + 32, a.rot_width, a.log2_base);
     }
-    for (int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < a.tokens; t += warps) {
+    // (unsigned: the step past the last of 2^31 - 1 tokens stays in front of 2^32)
+    for (unsigned t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < (unsigned)a.tokens; t += warps) {
         const int slot = a.slots[t];
         const int pos = a.rot_count > 0 ? a.pos[t] : 0;
         const bool valid = slot >= 0 && slot < a.num_slots;

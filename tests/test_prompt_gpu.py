@@ -1119,3 +1119,19 @@ def test_expand_and_append_at_once_on_two_streams(dev):
     torch.cuda.synchronize()
     for y in got:
         assert all(torch.equal(one[k].view(torch.int16), y[k].view(torch.int16)) for k in one)
+
+
+def test_append_of_as_many_tokens_as_there_are_numbers(dev):
+    """2^31 - 1 rows of 16 bytes, all but the last few skipped: the walk over them ends where they do."""
+    import torch
+    n = 2 ** 31 - 1
+    rows = torch.empty(n, 8, dtype=torch.bfloat16, device=dev)
+    slots = torch.full((n,), -1, dtype=torch.int32, device=dev)
+    tail = torch.arange(24, device=dev).view(3, 8).to(torch.bfloat16)
+    rows[-3:], slots[-3:] = tail, i32([5, 70, 127], dev)
+    cache, err = torch.zeros(2, 64, 8, dtype=torch.bfloat16, device=dev), word(dev)
+    p = K.make_params(1, 4, 1, 8, 0, 2, 2, 0)
+    K.append_slots_tensor(K.KVATTN_MLA, p, rows, None, slots, cache, 0.0, err)
+    want = torch.zeros(128, 8, dtype=torch.bfloat16, device=dev)
+    want[[5, 70, 127]] = tail
+    assert torch.equal(cache.view(128, 8), want) and int(err.item()) == 0
