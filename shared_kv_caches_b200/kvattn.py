@@ -346,7 +346,7 @@ def _dense(t, dtype, dims, index, what):
 def _last_axis(t, dtype, dims, index, what):
     """The strides of a tensor whose last axis is contiguous."""
     s = _check(t, dtype, dims, index, what).stride()
-    if s[-1] != 1 or 0 in s:
+    if s[-1] != 1 or (0 in s and any(x == 0 and n > 1 for x, n in zip(s, t.shape))):
         raise ValueError(f"{what}: the last axis is not contiguous, or an axis is broadcast")
     return s
 

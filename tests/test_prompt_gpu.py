@@ -1135,3 +1135,15 @@ def test_append_of_as_many_tokens_as_there_are_numbers(dev):
     want = torch.zeros(128, 8, dtype=torch.bfloat16, device=dev)
     want[[5, 70, 127]] = tail
     assert torch.equal(cache.view(128, 8), want) and int(err.item()) == 0
+
+
+def test_prefill_axes_of_one_element_may_have_a_stride_of_zero(dev):
+    """One head or one token, with the stride that a broadcast view gives its axis."""
+    rng = np.random.default_rng(34)
+    for ql, kl in (([1], [1]), ([5], [70])):
+        x = prefill_case(rng, 1, 1, 64, 16, 64, ql, kl, slack=0)
+        t = {k: up(v, dev) for k, v in x.items()}
+        one = {k: v.as_strided(v.shape, [0 if n == 1 else s for n, s in zip(v.shape, v.stride())]) for k, v in t.items()}
+        assert all(0 in v.stride() for k, v in one.items() if k != "kr")
+        got = K.prefill_tensors(one["q"], one["qr"], one["k"], one["kr"], one["v"], i32(starts(ql), dev), i32(starts(kl), dev), 0.1)
+        check_prefill(got, x, ql, kl, 0.1, True)
