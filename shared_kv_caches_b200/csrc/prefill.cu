@@ -736,10 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // one may be stored before the guard has taken it, and the other
             // query tile's may still be written.
             const int noted = n > 0 ? n - it->all / kKeys : 0;
-            uint32_t any_bad = 0;
-            for (int e = lane; e < noted * (kKeys / 32); e += 32)
-                any_bad |= B.bad[taken % kItems][e / (kKeys / 32)][e % (kKeys / 32)];
-            any_bad = __any_sync(0xffffffffu, any_bad != 0);
+            static_assert(kEdgeTiles * (kKeys / 32) <= 32, "a word of the notes a lane");
+            const bool any_bad =
+                __any_sync(0xffffffffu, lane < noted * (kKeys / 32) &&
+                                            B.bad[taken % kItems][lane / (kKeys / 32)][lane % (kKeys / 32)] != 0);
             const bool any = n > 0 && l != 0.f;          // a row without keys has l = 0 (NaN passes)
             const float inv = any ? 1.f / l : 0.f;
             const long long at = grow * a.out_token_stride + head * a.out_head_stride;
