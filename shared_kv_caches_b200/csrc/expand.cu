@@ -119,7 +119,7 @@ struct ExpandArgs {
     const __nv_bfloat16 *cache;
     __nv_bfloat16 *k, *v, *k_rope;
     int32_t *err;
-    int heads, heads_per_group, groups, branches, pairs_per_group, d_c, d_k, d_v, d_rope, row;
+    int heads_per_group, groups, branches, pairs_per_group, d_c, d_k, d_v, d_rope, row;
     int mpps, num_pages, max_kv;
 };
 
@@ -600,7 +600,6 @@ extern "C" int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const v
     a.v = static_cast<__nv_bfloat16 *>(v);
     a.k_rope = static_cast<__nv_bfloat16 *>(k_rope);
     a.err = device_error;
-    a.heads = pr.H;
     a.heads_per_group = pr.HPU;
     a.groups = pr.NU;
     a.branches = pr.mlra ? pr.NU : 1;
