@@ -376,6 +376,9 @@ int kvattn_head_proj(const void *x, const void *w, void *y, int32_t out_dtype, i
  * slots, write its rows, expand the cached latents and attend them.  In one
  * step: kvattn_build_tables, kvattn_append_slots, kvattn_expand_kv,
  * kvattn_prefill; then kvattn_decode token by token on the same cache.
+ * Row counts are host numbers and may be bounds: a step that reads nothing back
+ * (a captured one) passes the most rows that it can have, and the rows behind
+ * the last sequence are left alone.
  *
  * A ragged batch packs its sequences' rows one after the other: sequence b has
  * the rows [start[b], start[b + 1]) (int32 [batch + 1] on the device,
@@ -438,8 +441,8 @@ int kvattn_build_tables(int32_t batch, int32_t max_pages_per_seq, int32_t num_pa
  * pos[token] (any value) exactly as kvattn_rope does; rope_base = 0 stores the
  * rows as given (pos may be NULL; GTA takes only 0).
  * cache_dtype FP8_E4M3 (GQA): keys (turned) are divided by k_scale and values
- * by v_scale, rounded to the nearest e4m3 (ties to even) and saturated at
- * +-448; NaN stays NaN.
+ * by v_scale (the quotient in fp32), rounded to the nearest e4m3 (ties to even)
+ * and saturated at +-448; NaN stays NaN.
  * new_kv and kv_cache 16-byte aligned.
  */
 int kvattn_append_slots(int32_t variant, const kvattn_params *p, const void *new_kv, int32_t num_tokens,
@@ -488,6 +491,10 @@ int kvattn_expand_kv(int32_t variant, const kvattn_params *p, const void *kv_cac
  * causal = 1: query i of nq attends keys j <= i + nk - nq (the chunk is the
  * newest nq of the sequence's nk tokens); a query without keys gives out = 0,
  * lse = -inf.  causal = 0: every query attends every key.
+ * Keys and values are contiguous rows, not pages: for the latent variants those
+ * that kvattn_expand_kv writes.  No call reads the pages of a GQA, MQA or GTA
+ * cache (bf16 or fp8) for many query tokens: a chunk behind a cached past needs
+ * that past's keys and values as rows too.
  *
  * Strides in elements, {between tokens, between heads}; 0 takes that of the dense
  * layout: q_nope [T][QH][d_nope], q_rope [T][H][d_rope], out [T][H][d_v], and

@@ -19,9 +19,10 @@
 // latents in place and a head's weights read once for two tiles, an SM reads
 // 32 bytes a cycle from L2 while its MMAs run; one CTA on its own needs 64, and
 // the 96 KB that it can have in flight are then no more than the latency
-// times that (ragged MLA prompts, 22 thousand tokens: 818 us; so, 681).  Every cluster takes the same number of
-// (tile pair, group, head pair) units, in order, and loads latents only where
-// the tiles or the group change.
+// times that (ragged MLA prompts, 22 thousand tokens, calls repeated back to
+// back: 818 us; so, 678).  Every cluster takes the same number of (tile pair,
+// group, head pair) units, in order, and loads latents only where the tiles or
+// the group change.
 #include <math.h>
 
 #include "ragged.cuh"
@@ -139,8 +140,8 @@ __device__ __forceinline__ int page_or_none(const ExpandArgs &a, int seq, int pi
 }
 
 // L2 keeps the weights, which every cluster reads again for every tile pair,
-// rather than the outputs, which are more than it holds (GLA 16K 360 -> 332 us,
-// ragged MLA prompts 596 -> 590).
+// rather than the outputs, which are more than it holds (calls repeated back
+// to back: GLA 16K 393 -> 360 us, ragged MLA prompts 701 -> 678).
 __device__ __forceinline__ uint64_t keep_policy()
 {
     uint64_t p;

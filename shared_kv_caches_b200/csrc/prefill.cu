@@ -17,8 +17,8 @@
 // free as soon as they are in registers), and the other query tile's MMAs fill
 // what is left.  Measured: 1150 cycles per key tile and query tile (1056 of
 // MMAs) in the middle of an 8K prompt; the whole call, causal, 128 heads, takes
-// 1.90 ms from a cold start (1.45 PFLOP/s) and 2.2 ms when repeated, at the power
-// cap.
+// 2.24 ms when repeated back to back, at the power cap (1.23 PFLOP/s), and 1.95
+// to 2.0 ms for the first few calls after a pause.
 // Forming a part of the exponentials on the FMA pipe makes the softmax shorter
 // and the call longer (8K prompt 2263 us without, 2321 with a quarter of them).
 //
@@ -49,8 +49,8 @@
 // CTAs, one per SM, take its items as they get to them, ordered by groups of
 // eight heads, then tiles, then heads, so that the CTAs at work share a few
 // heads' keys and values in L2.  The last group is 16 heads or more: the items
-// handed out last are then short ones (4K prompt, 74 heads: 336 us with eight,
-// 313; 24 heads or more gain there and lose on longer prompts).
+// handed out last are then short ones (4K prompt, 74 heads, repeated: 378 us with
+// eight, 370; 24 heads or more gain there and lose on longer prompts).
 #include <math.h>
 
 #include <atomic>
