@@ -85,6 +85,7 @@ constexpr int kLaunchRegs = 168, kIssueRegs = 88, kSoftmaxRegs = 208;
 static_assert(kIssueRegs + 2 * kSoftmaxRegs <= 3 * kLaunchRegs, "register split");
 constexpr int kQBox = kTile * 128;                // 128 query rows x 64 bf16
 constexpr int kBox = kKeys * 128;                 // 96 keys x 64 bf16
+constexpr float kFarReference = 1073741824.f;     // 2^30
 constexpr int kHeadGroup = 8, kLastHeads = 16;    // heads of a group, and at least in the last one
 constexpr int kBarBytes = 2048;
 constexpr int kSmemMax = 227 * 1024;
@@ -677,7 +678,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     m_ref = mt;
                 }
-                const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                // Past 2^30 the reference's own rounding is 64 or more, and the
+                // FMA, which has c * s exactly, would turn that into 2^64: there
+                // (hardly ever) the raw maximum comes off first.
+                const bool far = fabsf(nm) > kFarReference;
+                if (__any_sync(0xffffffffu, far)) {
+                    const float off = far && e != -INFINITY ? e : 0.f;
+                    nm = far ? mt - m_ref : nm;
+#pragma unroll
+                    for (int y = 0; y < kKeys; ++y)
+                        s[y] -= off;
+                }
                 float sx[4] = {0.f, 0.f, 0.f, 0.f}, sy[4] = {0.f, 0.f, 0.f, 0.f};
                 uint32_t pk[kKeys / 2];
 #pragma unroll

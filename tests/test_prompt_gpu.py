@@ -1147,3 +1147,29 @@ def test_prefill_axes_of_one_element_may_have_a_stride_of_zero(dev):
         assert all(0 in v.stride() for k, v in one.items() if k != "kr")
         got = K.prefill_tensors(one["q"], one["qr"], one["k"], one["kr"], one["v"], i32(starts(ql), dev), i32(starts(kl), dev), 0.1)
         check_prefill(got, x, ql, kl, 0.1, True)
+
+
+@pytest.mark.parametrize("low", [-1e37, 1e36, -3e9, 1.5 * 2.0 ** 29])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_rows_whose_scores_are_all_far_from_zero(dev, low, causal):
+    """Every key that some rows attend scores the same number far from zero (a mask of a type's lowest value, written
+    into the keys): those rows weigh their keys alike.  Scores are one exact product, the weights 1 up to 2^64 on both
+    sides; 400 fp32 additions and the output's rounding as in the test of scale 0, the lse that of one rounding of the
+    score (2^-22 of it).  Rows of the other head, with common scores, keep their bits."""
+    rng = np.random.default_rng(35)
+    nq, nk = 200, 400
+    x = prefill_case(rng, 2, 2, 64, 0, 64, [nq], [nk])
+    plain = call(dev, x, [nq], [nk], 0.125, causal)
+    q, k = f64(x["q"]), f64(x["k"])
+    q[:nq, 0], k[0, :nk] = 0.0, 0.0
+    q[:nq, 0, 3], k[0, :nk, 3] = 2.0 ** 20, low / 2.0 ** 20 * 8
+    x["q"], x["k"] = W.f32_to_bf16_bits(q.astype(np.float32)), W.f32_to_bf16_bits(k.astype(np.float32))
+    score = 0.125 * f64(x["q"])[0, 0, 3] * f64(x["k"])[0, 0, 3]
+    got = call(dev, x, [nq], [nk], 0.125, causal)
+    out, lse, v = down(got["out"]), down(got["lse"]), f64(x["v"][0, :nk])
+    for i in range(nq):
+        n = i + nk - nq + 1 if causal else nk
+        want, mass = v[:n].mean(0), np.abs(v[:n]).mean(0)
+        assert np.all(np.abs(out[i, 0] - want) <= BF16 * np.abs(want) + 2.0 ** -13 * mass)
+        assert abs(lse[i, 0] - (score + np.log(n))) <= 2.0 ** -22 * abs(score) + 2.0 ** -14
+    assert np.array_equal(out[:nq, 1], down(plain["out"])[:nq, 1]) and np.array_equal(lse[:nq, 1], down(plain["lse"])[:nq, 1])
